@@ -271,6 +271,102 @@ nvfp4_status mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, int64_t
                         const uint8_t *b_scales, int64_t N, int64_t K, void *c, int64_t ldc, void *workspace,
                         size_t workspace_bytes, void *stream);
 
+/* ---- The operators around a layer's products ------------------------------------------
+ * (rows of the same library; the pages name the layers these sit in, not their formulas,
+ * which are the usual ones and are written out here.) */
+
+/* The form in which nvfp4_rms_norm and nvfp4_silu_mul write a rows x cols result v.
+ *  BF16:  BF16 values, row stride ld_out elements.  Any cols >= 1, any strides, 2-byte
+ *         alignment; 16-byte aligned pointers with cols % 16 == 0 and strides % 8 == 0 run
+ *         faster.
+ *  MXFP8: E4M3 codes, dense (rows, cols) bytes, and one E8M0 byte per 32 values
+ *         (mxfp4_scales_bytes(rows, cols, layout) bytes; OCP Microscaling Formats v1.0:
+ *         shared exponent floor(log2 amax) - 8 clamped to [-127, 127], -127 for an
+ *         all-zero block; elements rounded to nearest even, saturating at 448).
+ *  MXFP4: as mxfp4_quantize writes.
+ *  NVFP4: as nvfp4_quantize writes with ABSMAX block scales.
+ * The block formats take v in FP32 (no BF16 rounding in between), cols % 32 == 0 (NVFP4:
+ * % 16), 16-byte aligned pointers and input strides % 8 == 0; every scale byte is written,
+ * padding included.  A block that holds a NaN gets a NaN scale (E8M0 255, E4M3 0x7F). */
+typedef enum {
+    NVFP4_OUT_BF16 = 0,
+    NVFP4_OUT_MXFP8 = 1,
+    NVFP4_OUT_MXFP4 = 2,
+    NVFP4_OUT_NVFP4 = 3
+} nvfp4_out_format;
+
+/* Workspace nvfp4_rms_norm and nvfp4_silu_mul need (device memory, any content on entry)
+ * when they write NVFP4 without a given scale: 256 bytes.  Two calls that may run at the
+ * same time (other streams, other graphs) need a workspace each. */
+size_t nvfp4_row_workspace_bytes(void);
+
+/* Root-mean-square norm of a BF16 matrix, with the residual's addition before it:
+ *   h = BF16(x + residual)  (h = x without a residual), stored to residual_out;
+ *   v = (h r) (weight + weight_offset),  r = 1 / sqrt(mean over the row of h^2 + eps),
+ * sums and v in FP32.  The norm sees the rounded h, the value that the residual stream
+ * keeps, so the call equals an addition in BF16 followed by a norm.
+ *   x            device, BF16, rows x cols, row stride ld_x.
+ *   residual     device, BF16, rows x cols, row stride ld_residual, or NULL.
+ *   residual_out device, BF16, rows x cols, row stride ld_residual_out; NULL exactly when
+ *                residual is.  It may be residual or x itself (same pointer and stride).
+ *   weight       device, BF16, cols values, or NULL (ones, and weight_offset is not used).
+ *   weight_offset added to the weight in FP32 (1 for checkpoints that store weight - 1).
+ *   eps          finite, >= 0.
+ *   out          v in out_format (see there); BF16 may be written over x or residual_out's
+ *                input x (same pointer and stride).  ld_out is read for BF16 only.
+ *   layout, scales  the block formats' scales; NULL for BF16.
+ *   global_scale_in  NVFP4: device float > 0, the result's tensor scale, or NULL: amax / 2688
+ *                of v, computed on the device (1 for an all-zero result).  NULL otherwise.
+ *   global_scale_out NVFP4: device float or NULL, receives the tensor scale.
+ *   workspace    nvfp4_row_workspace_bytes() bytes; read only for NVFP4 without a given scale.
+ *   rows >= 0, rows <= 2^30; cols >= 1; the block formats: cols <= 65536 (SHAPE).
+ * Outputs must not overlap the inputs or one another except as stated (INVALID_ARG).
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, WORKSPACE, UNSUPPORTED_DEVICE, CUDA. */
+nvfp4_status nvfp4_rms_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, const void *residual,
+                            int64_t ld_residual, void *residual_out, int64_t ld_residual_out, const void *weight,
+                            float weight_offset, float eps, nvfp4_out_format out_format, nvfp4_sf_layout layout,
+                            const float *global_scale_in, void *out, int64_t ld_out, uint8_t *scales,
+                            float *global_scale_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The gate of a gated MLP, v = silu(gate) * up = gate / (1 + e^-gate) * up, in FP32.
+ *   gate, up     device, BF16, rows x cols each, row strides ld_gate, ld_up (the two halves
+ *                of one (rows, 2 cols) product are fine).
+ *   out, ...     as nvfp4_rms_norm; BF16 may be written over gate or up (same pointer and
+ *                stride).
+ *   rows >= 0, cols >= 1 (any cols; the block formats as in nvfp4_out_format).
+ * Errors as nvfp4_rms_norm. */
+nvfp4_status nvfp4_silu_mul(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int64_t rows,
+                            int64_t cols, nvfp4_out_format out_format, nvfp4_sf_layout layout,
+                            const float *global_scale_in, void *out, int64_t ld_out, uint8_t *scales,
+                            float *global_scale_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* y = x W^T for up to 16 tokens with x in 16 or 8 bits and W in NVFP4: the decode product
+ * that reads 4-bit weights without rounding the activation to 4 bits.
+ *   x            device, M x K, row stride ld_x elements: BF16 (x_scales NULL; ld_x % 8 == 0)
+ *                or E4M3 codes with their E8M0 scales (MXFP8; ld_x % 16 == 0).
+ *   x_scales     NULL, or device, the scales of M x K in layout x_layout, as nvfp4_rms_norm
+ *                and nvfp4_silu_mul write them (values finite in FP32).
+ *   w_codes, w_scales, w_global_scale  the weight N x K as nvfp4_quantize writes it (scales
+ *                SWIZZLED).
+ *   gate_codes, gate_scales, gate_global_scale  NULL, or a second N x K weight G:
+ *                y = silu(x G^T) * (x W^T), both products unrounded in FP32.
+ *   out          device BF16, M x N, row stride ld_out >= N (2-byte aligned, any stride).
+ *   0 <= M <= 16, N >= 1, K >= 32, K % 32 == 0.
+ * FP32 accumulation, no workspace, the same bits on every call.  Weights are exact; x is
+ * exact down to 2^-21 of the largest finite magnitude of its token (in the K range that a
+ * warp stages at a time), below that rounded at 2^-32 of it.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA. */
+nvfp4_status nvfp4_matvec(const void *x, const uint8_t *x_scales, nvfp4_sf_layout x_layout, int64_t M, int64_t K,
+                          int64_t ld_x, const uint8_t *w_codes, const uint8_t *w_scales,
+                          const float *w_global_scale, const uint8_t *gate_codes, const uint8_t *gate_scales,
+                          const float *gate_global_scale, int64_t N, void *out, int64_t ld_out, void *stream);
+
+/* nvfp4_matvec with MXFP4 weights, as mxfp4_quantize writes them (scales SWIZZLED).
+ * Weights of magnitude below 2^110 (larger ones may overflow the FP32 sums). */
+nvfp4_status mxfp4_matvec(const void *x, const uint8_t *x_scales, nvfp4_sf_layout x_layout, int64_t M, int64_t K,
+                          int64_t ld_x, const uint8_t *w_codes, const uint8_t *w_scales, const uint8_t *gate_codes,
+                          const uint8_t *gate_scales, int64_t N, void *out, int64_t ld_out, void *stream);
+
 /* Synchronize `stream` and read the device status word at the start of a GEMM
  * (or nvfp4_linear, nvfp4_linear_lora) workspace.  Returns NVFP4_OK when no bounded wait gave up, NVFP4_ERR_TIMEOUT
  * otherwise (and stores the raw word, which names the wait, in *word if non-NULL),
@@ -312,8 +408,9 @@ nvfp4_status nvfp4_quantize_noalloc(const void *x, int64_t rows, int64_t cols, i
                                     float *global_scale_out, float *block_err, void *stream);
 
 /* Number of kernels the most recent nvfp4_quantize / nvfp4_dequantize /
- * nvfp4_gemm call on the calling host thread enqueued (library bookkeeping for
- * launch counting; no counterpart on the pages). */
+ * nvfp4_gemm / nvfp4_rms_norm / nvfp4_silu_mul / nvfp4_matvec / mxfp4_matvec call
+ * on the calling host thread enqueued (library bookkeeping for launch counting; no
+ * counterpart on the pages). */
 int nvfp4_last_launch_count(void);
 
 #ifdef __cplusplus

@@ -30,17 +30,23 @@ SCALE_MSE = 1
 SCALE_FOUR_OVER_SIX = 2
 SF_SWIZZLED = 0
 SF_LINEAR = 1
+OUT_BF16 = 0
+OUT_MXFP8 = 1
+OUT_MXFP4 = 2
+OUT_NVFP4 = 3
+MATVEC_MAX_TOKENS = 16
 
 _MODES = {"absmax": SCALE_ABSMAX, "mse": SCALE_MSE, "four_over_six": SCALE_FOUR_OVER_SIX,
           SCALE_ABSMAX: SCALE_ABSMAX, SCALE_MSE: SCALE_MSE, SCALE_FOUR_OVER_SIX: SCALE_FOUR_OVER_SIX}
 _LAYOUTS = {"swizzled": SF_SWIZZLED, "linear": SF_LINEAR, SF_SWIZZLED: SF_SWIZZLED, SF_LINEAR: SF_LINEAR}
+_FORMATS = {"bf16": OUT_BF16, "mxfp8": OUT_MXFP8, "mxfp4": OUT_MXFP4, "nvfp4": OUT_NVFP4}
 
 STATUS = {0: "NVFP4_OK", 1: "NVFP4_ERR_INVALID_ARG", 2: "NVFP4_ERR_SHAPE", 3: "NVFP4_ERR_ALIGNMENT",
           4: "NVFP4_ERR_UNSUPPORTED_DEVICE", 5: "NVFP4_ERR_CUDA", 6: "NVFP4_ERR_TIMEOUT",
           7: "NVFP4_ERR_WORKSPACE"}
 
 # Every symbol include/nvfp4.h declares, with its ctypes signature.
-_P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_P, _I64, _SZ, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
     "nvfp4_status_string": ([_I], ctypes.c_char_p),
     "nvfp4_check_device": ([], _I),
@@ -60,6 +66,12 @@ SIGNATURES = {
     "mxfp4_quantize": ([_P, _I64, _I64, _I64, _I, _P, _P, _P], _I),
     "mxfp4_dequantize": ([_P, _P, _I, _I64, _I64, _P, _I64, _P], _I),
     "mxfp4_gemm": ([_P, _P, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _SZ, _P], _I),
+    "nvfp4_row_workspace_bytes": ([], _SZ),
+    "nvfp4_rms_norm": ([_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _F, _F, _I, _I, _P, _P, _I64, _P, _P, _P, _SZ,
+                        _P], _I),
+    "nvfp4_silu_mul": ([_P, _I64, _P, _I64, _I64, _I64, _I, _I, _P, _P, _I64, _P, _P, _P, _SZ, _P], _I),
+    "nvfp4_matvec": ([_P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _P], _I),
+    "mxfp4_matvec": ([_P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P], _I),
     "nvfp4_read_device_error": ([_P, _P, ctypes.POINTER(ctypes.c_uint32)], _I),
     "nvfp4_last_launch_count": ([], _I),
     "nvfp4_quantize_noalloc": ([_P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P], _I),
@@ -344,3 +356,220 @@ def mxfp4_gemm(a: MXFP4Tensor, b: MXFP4Tensor, out: Optional[torch.Tensor] = Non
     _check(lib.mxfp4_gemm(_ptr(a.codes), _ptr(a.scales), M, _ptr(b.codes), _ptr(b.scales), N, K, _ptr(out),
                           out.stride(0), _ptr(workspace), workspace.numel(), _stream(stream)), "mxfp4_gemm")
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# The operators around a layer's products: norm, gate, and the weight-only product of a few tokens
+# ---------------------------------------------------------------------------------------------
+
+@dataclass
+class MXFP8Tensor:
+    """A rows x cols tensor in MXFP8: E4M3 codes and one E8M0 scale per 32 values."""
+    codes: torch.Tensor   # float8_e4m3fn (rows, cols)
+    scales: torch.Tensor  # uint8, flat swizzled buffer or (rows, cols/32) linear
+    rows: int
+    cols: int
+    layout: int = SF_SWIZZLED
+
+
+class _On:
+    """The device and stream of one call on `tensor`: makes the tensor's device current, and where the caller
+    names a stream, allocates on it (a temporary is not reused before that stream is through with it)."""
+
+    def __init__(self, tensor: torch.Tensor, stream):
+        self.contexts = []
+        if tensor.device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(tensor.device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=tensor.device)
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _matrix(t: torch.Tensor, name: str, device=None, shape=None) -> int:
+    """Checks a BF16 matrix argument and returns its row stride (a single row's is its length, rounded up)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D bfloat16 CUDA tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major (stride 1 along its rows)")
+    return -(-cols // 16) * 16 if rows <= 1 else t.stride(0)
+
+
+def _like(t: Optional[torch.Tensor], name: str, dtype, numel: int, device) -> None:
+    if t is not None and (t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {device}")
+
+
+def _row_output(fmt: int, layout: int, rows: int, cols: int, device, out, global_scale):
+    """The output tensors of a row operator: (what the caller gets, data, row stride, scales, tensor scale)."""
+    if global_scale is not None:
+        if fmt != OUT_NVFP4:
+            raise ValueError("global_scale is NVFP4's tensor scale; this format has none")
+        _like(global_scale, "global_scale", torch.float32, 1, device)
+    if fmt == OUT_BF16:
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+        return out, out, _matrix(out, "out", device, (rows, cols)), None, None
+    block = 16 if fmt == OUT_NVFP4 else 32
+    if cols % block:
+        raise ValueError(f"{cols} columns are no whole number of {block}-value blocks")
+    lib = load_library()
+    nsf = (lib.nvfp4_scales_bytes if block == 16 else lib.mxfp4_scales_bytes)(rows, cols, layout)
+    kind = {OUT_MXFP8: MXFP8Tensor, OUT_MXFP4: MXFP4Tensor, OUT_NVFP4: NVFP4Tensor}[fmt]
+    width, dtype = (cols, torch.float8_e4m3fn) if fmt == OUT_MXFP8 else (cols // 2, torch.uint8)
+    if out is None:
+        codes = torch.empty((rows, width), dtype=dtype, device=device)
+        scales = torch.empty((rows, cols // block) if layout == SF_LINEAR else (nsf,), dtype=torch.uint8, device=device)
+        if fmt == OUT_NVFP4:
+            gs = torch.empty(1, dtype=torch.float32, device=device)
+            out = NVFP4Tensor(codes, scales, gs, rows, cols, layout)
+        else:
+            out = kind(codes, scales, rows, cols, layout)
+    else:
+        if not isinstance(out, kind) or (out.rows, out.cols, out.layout) != (rows, cols, layout):
+            raise ValueError(f"out must be a {kind.__name__} of {rows} x {cols} with the asked scale layout")
+        _like(out.codes, "out.codes", dtype, rows * width, device)
+        _like(out.scales, "out.scales", torch.uint8, nsf, device)
+        if fmt == OUT_NVFP4:
+            _like(out.global_scale, "out.global_scale", torch.float32, 1, device)
+    return out, out.codes, cols, out.scales, out.global_scale if fmt == OUT_NVFP4 else None
+
+
+def _row_workspace(fmt: int, global_scale, workspace, device):
+    """(workspace, its bytes): only NVFP4 with a computed tensor scale needs one."""
+    if workspace is None and fmt == OUT_NVFP4 and global_scale is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=device)
+    if workspace is None:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _choice(table, value, name):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {[k for k in table if isinstance(k, str)]}, got {value!r}") from None
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6, weight_offset: float = 0.0, out_format: str = "bf16", layout="swizzled",
+             global_scale: Optional[torch.Tensor] = None, out=None, residual_out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None, stream=None):
+    """Root-mean-square norm of the rows of a 2-D BF16 tensor, the residual's addition before it and the
+    quantizer behind it (see nvfp4_rms_norm in include/nvfp4.h):
+
+        h = BF16(x + residual);  v = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)
+
+    out_format: "bf16" -> a tensor, "mxfp8" -> MXFP8Tensor, "mxfp4" -> MXFP4Tensor, "nvfp4" -> NVFP4Tensor, whose
+    tensor scale is `global_scale` (a device float) or computed from v.  Returns the output, or with a residual
+    (output, h); residual_out may be `residual` itself to update the stream in place."""
+    fmt, lay = _choice(_FORMATS, out_format, "out_format"), _choice(_LAYOUTS, layout, "layout")
+    ld_x = _matrix(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    if (residual is None) and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight is not None:
+        _like(weight, "weight", torch.bfloat16, cols, dev)
+    with _On(x, stream):
+        result, data, ld_out, scales, gs = _row_output(fmt, lay, rows, cols, dev, out, global_scale)
+        ld_r = ld_ro = 0
+        if residual is not None:
+            ld_r = _matrix(residual, "residual", dev, x.shape)
+            if residual_out is None:
+                residual_out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+            ld_ro = _matrix(residual_out, "residual_out", dev, x.shape)
+        workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, dev)
+        _check(load_library().nvfp4_rms_norm(_at(x), rows, cols, ld_x, _at(residual), ld_r, _at(residual_out), ld_ro,
+                                             _at(weight), weight_offset, eps, fmt, lay, _at(global_scale), _at(data),
+                                             ld_out, _at(scales), _at(gs), _at(workspace), ws_bytes,
+                                             _raw_stream(dev)), "nvfp4_rms_norm")
+    return result if residual is None else (result, residual_out)
+
+
+def silu_mul(gate: torch.Tensor, up: torch.Tensor, out_format: str = "bf16", layout="swizzled",
+             global_scale: Optional[torch.Tensor] = None, out=None, workspace: Optional[torch.Tensor] = None,
+             stream=None):
+    """silu(gate) * up of two 2-D BF16 tensors (strided views, such as the halves of one product, are fine), written
+    as `out_format` like rms_norm's output (see nvfp4_silu_mul in include/nvfp4.h)."""
+    fmt, lay = _choice(_FORMATS, out_format, "out_format"), _choice(_LAYOUTS, layout, "layout")
+    ld_g = _matrix(gate, "gate")
+    rows, cols = gate.shape
+    dev = gate.device
+    ld_u = _matrix(up, "up", dev, gate.shape)
+    with _On(gate, stream):
+        result, data, ld_out, scales, gs = _row_output(fmt, lay, rows, cols, dev, out, global_scale)
+        workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, dev)
+        _check(load_library().nvfp4_silu_mul(_at(gate), ld_g, _at(up), ld_u, rows, cols, fmt, lay, _at(global_scale),
+                                             _at(data), ld_out, _at(scales), _at(gs), _at(workspace), ws_bytes,
+                                             _raw_stream(dev)), "nvfp4_silu_mul")
+    return result
+
+
+def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = x w^T in BF16 for up to MATVEC_MAX_TOKENS rows of x (2-D BF16 tensor, or MXFP8Tensor) and a 4-bit weight w
+    (NVFP4Tensor or MXFP4Tensor, N x K, swizzled scales); the activation is not rounded to 4 bits.  With w_gate, a
+    second weight of the same kind and shape: silu(x w_gate^T) * (x w^T) in one pass.  More rows: use linear,
+    nvfp4_gemm or mxfp4_gemm."""
+    fp8 = isinstance(x, MXFP8Tensor)
+    dev = x.codes.device if fp8 else x.device
+    if fp8:
+        if not x.codes.is_cuda:
+            raise ValueError("x must be on a CUDA device")
+        M, K, ld_x, x_lay = x.rows, x.cols, x.cols, _choice(_LAYOUTS, x.layout, "x.layout")
+        _like(x.codes, "x.codes", torch.float8_e4m3fn, M * K, dev)
+        _like(x.scales, "x.scales", torch.uint8, mxfp8_scales_bytes(M, K, x_lay), dev)
+        xd, xs = x.codes, x.scales
+    else:
+        ld_x = _matrix(x, "x")
+        (M, K), xd, xs, x_lay = x.shape, x, None, SF_SWIZZLED
+    nvfp4 = isinstance(w, NVFP4Tensor)
+    if not nvfp4 and not isinstance(w, MXFP4Tensor):
+        raise ValueError("w must be an NVFP4Tensor or an MXFP4Tensor")
+    N = w.rows
+    for t in (w,) if w_gate is None else (w, w_gate):
+        if type(t) is not type(w) or (t.rows, t.cols) != (N, K) or t.layout != SF_SWIZZLED or t.codes.device != dev:
+            raise ValueError("the weights must share K with x, one kind and shape, x's device, and have swizzled scales")
+    with _On(xd, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        ld_out = max(_matrix(out, "out", dev, (M, N)), N)
+        lib, s = load_library(), _raw_stream(dev)
+        gc, gsc = (None, None) if w_gate is None else (w_gate.codes.data_ptr(), w_gate.scales.data_ptr())
+        if nvfp4:
+            gg = None if w_gate is None else w_gate.global_scale.data_ptr()
+            st = lib.nvfp4_matvec(xd.data_ptr(), _at(xs), x_lay, M, K, ld_x, w.codes.data_ptr(), w.scales.data_ptr(),
+                                  w.global_scale.data_ptr(), gc, gsc, gg, N, out.data_ptr(), ld_out, s)
+        else:
+            st = lib.mxfp4_matvec(xd.data_ptr(), _at(xs), x_lay, M, K, ld_x, w.codes.data_ptr(), w.scales.data_ptr(),
+                                  gc, gsc, N, out.data_ptr(), ld_out, s)
+        _check(st, "nvfp4_matvec" if nvfp4 else "mxfp4_matvec")
+    return out
+
+
+def mxfp8_scales_bytes(rows: int, cols: int, layout=SF_SWIZZLED) -> int:
+    """Bytes of an MXFP8 tensor's E8M0 scales (the layouts are MXFP4's: one byte per 32 values)."""
+    return load_library().mxfp4_scales_bytes(rows, cols, _LAYOUTS[layout])

@@ -1,0 +1,625 @@
+// row_ops.cu -- the operators around a layer's products, with the quantizer fused in:
+//   rms_norm: h = BF16(x + residual) (kept as the new residual stream),
+//             v = (h r)(w + offset), r = 1/sqrt(mean(h^2) + eps);
+//   silu_mul: v = g / (1 + e^-g) * u;
+// and v leaves as BF16, MXFP8, MXFP4 or NVFP4.  The block scales and codes are taken
+// from v in binary32, not from a BF16 copy of it, so a block format rounds once.
+//
+// Formats (per block of the row, all binary32 round-to-nearest-even):
+//   MXFP8 / MXFP4 (OCP Microscaling Formats v1.0): 32 values, shared exponent
+//     floor(log2 amax) - 8 (E4M3 elements) or - 2 (E2M1), clamped to [-127, 127], -127 for
+//     an all-zero block; scale byte 255 (NaN) for a block that holds a NaN;
+//   NVFP4: the absmax rule of the quantizer: s_b = E4M3(amax_b / (6 s_g)), codes
+//     E2M1(v * RN(1 / (s_b s_g))), s_g given or amax / 2688 over the whole output
+//     (1 for an all-zero one).  A block that holds a NaN has a NaN scale.
+//
+// One thread owns 16 consecutive values (two 16-byte loads): an NVFP4 block, or half
+// an MX block (the pair of lanes shares its maximum with one shuffle).
+#include <cuda_runtime.h>
+
+#include "../../include/nvfp4.h"
+#include "layer_ops.h"
+#include "ptx.cuh"
+#include "quant_block.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kUnit = 16;       // values per thread step
+constexpr int kCluster = 8;     // CTAs that share one amax through distributed shared memory
+// Threads per row and units per thread of norm_kernel: U = 1 up to 1024 threads, U = 2,
+// 4, 8 up to 512 (64 or 128 registers each); the longest row is 8 x 512 units.
+constexpr int norm_threads(int U) { return U == 1 ? 1024 : 512; }
+constexpr int64_t kNormMaxCols = 8 * 512 * kUnit;
+
+// The phases of an operator whose NVFP4 tensor scale is computed from its own output.
+enum Phase {
+  kOnePass,  // the scale is given, or the format has none
+  kCluster1, // one cluster: amax through distributed shared memory, then the output
+  kAmax,     // first of two launches: (residual stream and) amax
+  kFormat    // second launch: the output, under the amax word of the first
+};
+
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// two floats -> BF16 pair, a in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+
+// two floats -> E4M3 pair (saturating, NaN kept), a in the low byte
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
+  return d;
+}
+
+// The sixteen BF16 values of a thread's unit as floats.
+__device__ __forceinline__ void widen(const uint32_t (&w)[8], float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ void load_unit(const uint16_t* p, uint32_t (&w)[8]) {
+  const uint4 a = ld_v4(p), b = ld_v4(p + 8);
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+__device__ __forceinline__ void store_unit(uint16_t* p, const uint32_t (&w)[8]) {
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__device__ __forceinline__ float amax16(const float (&v)[16]) {
+  float m = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) m = max_nan(m, fabsf(v[i]));
+  return m;
+}
+
+// s_g of an output whose largest magnitude is amax
+__device__ __forceinline__ float tensor_scale(float amax) { return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 2688.0f); }
+
+// shared exponent of an MX block: floor(log2 amax) - emax, clamped (amax = 0: -127)
+__device__ __forceinline__ int mx_exponent(float amax, int emax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int e = static_cast<int>(bits >> 23);
+  const int lg = e > 0 ? e - 127 : (31 - __clz(static_cast<int>(bits))) - 149;
+  return bits == 0u ? -127 : max(-127, min(127, lg - emax));
+}
+
+__device__ __forceinline__ float exp2_int(int k) {  // k in [-127, 127]
+  return k >= -126 ? __uint_as_float(static_cast<uint32_t>(k + 127) << 23) : __uint_as_float(0x00400000u);
+}
+
+// Writes unit u (values 16 u .. 16 u + 15) of row r.  Every lane of the warp calls it
+// with u = a multiple of 32 + lane; `active`: u is inside the row.
+template <int FMT>
+__device__ __forceinline__ void emit(const float (&v)[16], int64_t r, int64_t u, bool active, int64_t cols, float sg,
+                                     const RowOutput& o) {
+  if constexpr (FMT == NVFP4_OUT_BF16) {
+    if (!active) return;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    store_unit(static_cast<uint16_t*>(o.out) + r * o.ld_out + u * kUnit, w);
+  } else {
+    const int lane = threadIdx.x & 31;
+    constexpr int kLanes = FMT == NVFP4_OUT_NVFP4 ? 1 : 2;  // lanes per block
+    const int64_t nblk = cols / (kUnit * kLanes);
+    float amax = active ? amax16(v) : 0.0f;
+    uint32_t sbyte = 0;
+    if constexpr (FMT == NVFP4_OUT_NVFP4) {
+      sbyte = cvt_e4m3_satfinite(__fdiv_rn(amax, __fmul_rn(6.0f, sg)));
+      if (active) {
+        const float eff = __fmul_rn(e4m3_to_float(sbyte), sg);
+        uint64_t x2[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x2[i] = pack2(v[2 * i], v[2 * i + 1]);
+        uint32_t c0, c1;
+        encode_codes(x2, eff, __frcp_rn(eff), c0, c1);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(o.out) + r * (cols / 2) + u * 8) = make_uint2(c0, c1);
+      }
+    } else {
+      amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      const int e = mx_exponent(amax, FMT == NVFP4_OUT_MXFP8 ? 8 : 2);
+      sbyte = amax != amax ? 255u : static_cast<uint32_t>(e + 127);
+      const float inv = exp2_int(-e);
+      if (active) {
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(v[i], inv);
+        if constexpr (FMT == NVFP4_OUT_MXFP8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack_e4m3(y[4 * i], y[4 * i + 1]) | (pack_e4m3(y[4 * i + 2], y[4 * i + 3]) << 16);
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(o.out) + r * cols + u * 16) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          const uint32_t c0 = cvt_e2m1x8(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
+          const uint32_t c1 = cvt_e2m1x8(y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(o.out) + r * (cols / 2) + u * 8) = make_uint2(c0, c1);
+        }
+      }
+    }
+    const int64_t b = u / kLanes;
+    if (o.swizzled) {
+      // four consecutive blocks' bytes in one 32-bit store; a block past the row's end
+      // is the tile's padding and contributes 0
+      if (!active) sbyte = 0;
+      const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, sbyte, kLanes);
+      const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, sbyte, 2 * kLanes);
+      const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, sbyte, 3 * kLanes);
+      if (active && (lane % (4 * kLanes)) == 0) {
+        const int64_t atoms = (nblk + 3) / 4;
+        const int64_t at = ((r >> 7) * atoms + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+        *reinterpret_cast<uint32_t*>(o.scales + at) = sbyte | (s1 << 8) | (s2 << 16) | (s3 << 24);
+      }
+    } else if (active && (lane % kLanes) == 0) {
+      o.scales[r * nblk + b] = static_cast<uint8_t>(sbyte);
+    }
+  }
+}
+
+// Zeroes the row padding of a swizzled scale buffer: the 16-byte lines of its last row
+// group (rows q * 32 + line of the group in word q), by threads `tid` of `threads`.
+__device__ __forceinline__ void zero_row_padding(uint8_t* scales, int64_t rows, int64_t nblk, int64_t tid,
+                                                 int64_t threads) {
+  const int64_t tail = rows & 127;
+  if (tail == 0) return;
+  const int64_t atoms = (nblk + 3) / 4;
+  uint8_t* base = scales + (rows >> 7) * atoms * 512;
+  for (int64_t i = tid; i < atoms * 32; i += threads) {
+    uint32_t* line = reinterpret_cast<uint32_t*>(base + i * 16);
+    const int64_t l = i & 31;
+    if (l >= tail) {
+      *reinterpret_cast<uint4*>(line) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+#pragma unroll
+      for (int q = 1; q < 4; ++q)
+        if (l + 32 * q >= tail) line[q] = 0u;
+    }
+  }
+}
+
+// 16-byte lines that a padding CTA of `threads` threads zeroes per thread, and the CTAs needed.
+int64_t padding_lines(int64_t rows, int64_t cols, const RowOutput& o) {
+  if (o.format == NVFP4_OUT_BF16 || !o.swizzled || (rows & 127) == 0) return 0;
+  const int64_t nblk = cols / (o.format == NVFP4_OUT_NVFP4 ? 16 : 32);
+  return (nblk + 3) / 4 * 32;
+}
+
+__device__ __forceinline__ float cluster_max(float mine, float* slot) {
+  // mine >= 0 or NaN: the bit patterns order like the values, NaN above all
+  if (threadIdx.x == 0) *slot = mine;
+  cluster_sync();
+  uint32_t g = 0;
+  for (uint32_t i = 0; i < static_cast<uint32_t>(kCluster); ++i)
+    g = max(g, ld_shared_cluster_u32(mapa_shared(smem_u32(slot), i)));
+  cluster_sync();  // no CTA leaves while another still reads its word
+  return __uint_as_float(g);
+}
+
+// Sum over the CTA (every thread gets it), in a fixed order.  One __syncthreads; `part`
+// must not be reused before another one.
+__device__ __forceinline__ float block_sum(float s, float* part) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (lane == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = lane < nw ? part[lane] : 0.0f;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+  return s;
+}
+
+// Maximum over the CTA of a magnitude (>= 0 or NaN) as its bit pattern; valid in every thread.
+__device__ __forceinline__ float block_max(float m, uint32_t* part) {
+  uint32_t b = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m) & 0x7FFFFFFFu);
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (lane == 0) part[threadIdx.x >> 5] = b;
+  __syncthreads();
+  b = __reduce_max_sync(0xFFFFFFFFu, lane < nw ? part[lane] : 0u);
+  return __uint_as_float(b);
+}
+
+__device__ __forceinline__ float inv_rms(float sum_sq, int64_t cols, float eps) {
+  return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum_sq, static_cast<float>(cols)), eps));
+}
+
+// One CTA per row; thread t owns units t, t + T, ... (U of them), kept in registers
+// between the sum of squares and the output, so each input is read once.
+template <int FMT, int U, int PHASE>
+__global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a, const RowOutput o) {
+  __shared__ float sums[32];
+  __shared__ uint32_t maxima[32];
+  __shared__ float cta_max;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t units = a.cols / kUnit;
+  const int T = blockDim.x;
+  if (PHASE != kCluster1 && blockIdx.x >= a.rows) {  // a padding CTA
+    zero_row_padding(o.scales, a.rows, a.cols / (FMT == NVFP4_OUT_NVFP4 ? 16 : 32),
+                     (static_cast<int64_t>(blockIdx.x) - a.rows) * T + threadIdx.x,
+                     (static_cast<int64_t>(gridDim.x) - a.rows) * T);
+    return;
+  }
+  // the second launch walks the rows backwards: the last rows of the first are in L2
+  const int64_t r = PHASE == kFormat ? a.rows - 1 - blockIdx.x : blockIdx.x;
+  const bool row = PHASE != kCluster1 || r < a.rows;
+  uint32_t h[U][8];
+  float s = 0.0f;
+  const bool add = PHASE != kFormat && a.residual != nullptr;
+  const uint16_t* src = PHASE == kFormat && a.residual ? a.residual_out + r * a.ld_res_out : a.x + r * a.ld_x;
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
+    if (row && u < units) {
+      load_unit(src + u * kUnit, h[k]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] = 0u;
+    }
+  }
+  if (add && U > 4) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
+      if (row && u < units) {
+        uint32_t q[8];
+        load_unit(a.residual + r * a.ld_res + u * kUnit, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          h[k][i] = pack_bf16(bf16_lo(h[k][i]) + bf16_lo(q[i]), bf16_hi(h[k][i]) + bf16_hi(q[i]));
+        store_unit(a.residual_out + r * a.ld_res_out + u * kUnit, h[k]);
+      }
+    }
+  } else if (add) {  // all loads of the residual in flight together
+    uint32_t q[U][8];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
+      if (row && u < units) load_unit(a.residual + r * a.ld_res + u * kUnit, q[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
+      if (row && u < units) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          h[k][i] = pack_bf16(bf16_lo(h[k][i]) + bf16_lo(q[k][i]), bf16_hi(h[k][i]) + bf16_hi(q[k][i]));
+        store_unit(a.residual_out + r * a.ld_res_out + u * kUnit, h[k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    float v[16];
+    widen(h[k], v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s = __fmaf_rn(v[i], v[i], s);
+  }
+  const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
+
+  auto values = [&](int k, float (&v)[16]) {
+    const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
+    widen(h[k], v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], rstd);
+    if (a.weight != nullptr && u < units) {
+      uint32_t w[8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.weight + u * kUnit) + half);
+        w[4 * half] = q.x, w[4 * half + 1] = q.y, w[4 * half + 2] = q.z, w[4 * half + 3] = q.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[2 * i] = __fmul_rn(v[2 * i], __fadd_rn(bf16_lo(w[i]), a.weight_offset));
+        v[2 * i + 1] = __fmul_rn(v[2 * i + 1], __fadd_rn(bf16_hi(w[i]), a.weight_offset));
+      }
+    }
+  };
+
+  float sg = 1.0f;
+  if constexpr (PHASE == kCluster1 || PHASE == kAmax) {
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      float v[16];
+      values(k, v);
+      if (row && threadIdx.x + static_cast<int64_t>(k) * T < units) m = max_nan(m, amax16(v));
+    }
+    m = block_max(m, maxima);
+    if constexpr (PHASE == kAmax) {
+      if (threadIdx.x == 0 && __float_as_uint(m) != 0u) atomicMax(o.amax_word, __float_as_uint(m));
+      return;
+    }
+    sg = tensor_scale(cluster_max(m, &cta_max));
+  } else if constexpr (FMT == NVFP4_OUT_NVFP4) {
+    sg = PHASE == kFormat ? tensor_scale(__uint_as_float(*o.amax_word)) : *o.gs_in;
+  }
+  if (FMT == NVFP4_OUT_NVFP4 && o.gs_out && blockIdx.x == 0 && threadIdx.x == 0) *o.gs_out = sg;
+  if (row) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
+      if (U > 1 && u - threadIdx.x >= units) break;
+      float v[16];
+      values(k, v);
+      emit<FMT>(v, r, u, u < units, a.cols, sg, o);
+    }
+  }
+  if (PHASE == kCluster1 && o.swizzled)
+    zero_row_padding(o.scales, a.rows, a.cols / 16, static_cast<int64_t>(blockIdx.x) * T + threadIdx.x,
+                     static_cast<int64_t>(gridDim.x) * T);
+}
+
+// BF16 rows that the 16-value units do not fit (odd sizes, strides or addresses, or rows
+// longer than a CTA's registers hold): one value per thread and step, the second pass
+// re-reads h (each thread its own values, so x may be the output).
+__global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_t* out, int64_t ld_out) {
+  __shared__ float sums[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t r = blockIdx.x;
+  const uint16_t* x = a.x + r * a.ld_x;
+  float s = 0.0f;
+  if (a.residual) {
+    const uint16_t* q = a.residual + r * a.ld_res;
+    uint16_t* ho = a.residual_out + r * a.ld_res_out;
+    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+      const uint32_t h = pack_bf16(bf16_bits_to_float(x[c]) + bf16_bits_to_float(q[c]), 0.0f) & 0xFFFFu;
+      ho[c] = static_cast<uint16_t>(h);
+      const float f = bf16_bits_to_float(h);
+      s = __fmaf_rn(f, f, s);
+    }
+    x = ho;
+  } else {
+    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+      const float f = bf16_bits_to_float(x[c]);
+      s = __fmaf_rn(f, f, s);
+    }
+  }
+  const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
+  for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    float v = __fmul_rn(bf16_bits_to_float(x[c]), rstd);
+    if (a.weight) v = __fmul_rn(v, __fadd_rn(bf16_bits_to_float(a.weight[c]), a.weight_offset));
+    out[r * ld_out + c] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+  }
+}
+
+// g / (1 + e^-g) * u.  The quotient is refined to about half a unit in the last place, so
+// that the block formats' rounding borders see no more error than a plain binary32
+// evaluation has.  Where the refinement has no meaning (1 + e^-g or g infinite) its NaN
+// gives way to the first quotient, which is the IEEE one: 0, an infinity, or NaN.
+__device__ __forceinline__ float silu_times(float g, float u) {
+  const float d = __fadd_rn(1.0f, expf(-g));
+  float rc;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(d));
+  const float q0 = __fmul_rn(g, rc);
+  const float q = __fmaf_rn(__fmaf_rn(-d, q0, g), rc, q0);
+  return __fmul_rn(q == q ? q : q0, u);
+}
+
+// One warp per 32 consecutive units of a row.
+template <int FMT, int PHASE>
+__global__ void __launch_bounds__(256) gate_kernel(const GateArgs a, const RowOutput o) {
+  __shared__ uint32_t maxima[32];
+  __shared__ float cta_max;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t units = a.cols / kUnit;
+  const int64_t chunks = (units + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  // The warp's tasks: chunk c0 of row r0, then step_r rows and step_c chunks further,
+  // with a carry (no division per task).
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const int64_t r0 = warp / chunks, c0 = warp - r0 * chunks;
+  const int64_t step_r = warps / chunks, step_c = warps - step_r * chunks;
+  auto next = [&](int64_t& r, int64_t& c) {
+    r += step_r;
+    c += step_c;
+    if (c >= chunks) {
+      c -= chunks;
+      ++r;
+    }
+  };
+
+  auto load = [&](int64_t r, int64_t u, float (&v)[16]) {
+    const bool active = u < units;
+    uint32_t g[8], q[8];
+    if (active) {
+      load_unit(a.gate + r * a.ld_gate + u * kUnit, g);
+      load_unit(a.up + r * a.ld_up + u * kUnit, q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = q[i] = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = silu_times(bf16_lo(g[i]), bf16_lo(q[i]));
+      v[2 * i + 1] = silu_times(bf16_hi(g[i]), bf16_hi(q[i]));
+    }
+    return active;
+  };
+
+  float sg = 1.0f;
+  if constexpr (PHASE == kCluster1 || PHASE == kAmax) {
+    float m = 0.0f;
+    for (int64_t r = r0, c = c0; r < a.rows; next(r, c)) {
+      float v[16];
+      load(r, c * 32 + lane, v);  // an inactive lane's values are 0
+      m = max_nan(m, amax16(v));
+    }
+    m = block_max(m, maxima);
+    if constexpr (PHASE == kAmax) {
+      if (threadIdx.x == 0 && __float_as_uint(m) != 0u) atomicMax(o.amax_word, __float_as_uint(m));
+      return;
+    }
+    sg = tensor_scale(cluster_max(m, &cta_max));
+  } else if constexpr (FMT == NVFP4_OUT_NVFP4) {
+    sg = PHASE == kFormat ? tensor_scale(__uint_as_float(*o.amax_word)) : *o.gs_in;
+  }
+  if (FMT == NVFP4_OUT_NVFP4 && o.gs_out && blockIdx.x == 0 && threadIdx.x == 0) *o.gs_out = sg;
+  for (int64_t r = r0, c = c0; r < a.rows; next(r, c)) {
+    // the second launch walks backwards: the end of the first's reads is in L2
+    const int64_t rr = PHASE == kFormat ? a.rows - 1 - r : r;
+    const int64_t u = (PHASE == kFormat ? chunks - 1 - c : c) * 32 + lane;
+    float v[16];
+    const bool active = load(rr, u, v);
+    emit<FMT>(v, rr, u, active, a.cols, sg, o);
+  }
+  if (FMT != NVFP4_OUT_BF16 && o.swizzled)
+    zero_row_padding(o.scales, a.rows, a.cols / (FMT == NVFP4_OUT_NVFP4 ? 16 : 32),
+                     static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                     static_cast<int64_t>(gridDim.x) * blockDim.x);
+}
+
+// BF16 values that the 16-value units do not fit.
+__global__ void __launch_bounds__(256) gate_any_kernel(const GateArgs a, uint16_t* out, int64_t ld_out) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t n = a.rows * a.cols, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+    const int64_t r = i / a.cols, c = i - r * a.cols;
+    const float v = silu_times(bf16_bits_to_float(a.gate[r * a.ld_gate + c]),
+                               bf16_bits_to_float(a.up[r * a.ld_up + c]));
+    out[r * ld_out + c] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+  }
+}
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), int64_t grid, int threads, int cluster, cudaStream_t stream, int* launches,
+                   Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  return cudaGetLastError();
+}
+
+bool fits_units(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+
+template <int FMT, int PHASE>
+cudaError_t norm_launch_u(const NormArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
+  const int64_t units = a.cols / kUnit;
+  // Few rows: as many threads as a row has units, for the shortest chain of loads per
+  // thread; more rows than the SMs hold CTAs: two units per thread.
+  int U = a.rows <= 2 * 148 ? 1 : 2;
+  while (U < 8 && (units + U - 1) / U > norm_threads(U)) U *= 2;
+  int T = static_cast<int>(((units + U - 1) / U + 31) / 32 * 32);
+  if (T < 64) T = 64;
+  const int64_t pad = PHASE == kCluster1 || PHASE == kAmax ? 0 : padding_lines(a.rows, a.cols, o);
+  const int64_t grid = PHASE == kCluster1 ? kCluster : a.rows + (pad + T - 1) / T;
+  const int cluster = PHASE == kCluster1 ? kCluster : 1;
+  if (U == 1) return launch(norm_kernel<FMT, 1, PHASE>, grid, T, cluster, stream, launches, a, o);
+  if (U == 2) return launch(norm_kernel<FMT, 2, PHASE>, grid, T, cluster, stream, launches, a, o);
+  if (U == 4) return launch(norm_kernel<FMT, 4, PHASE>, grid, T, cluster, stream, launches, a, o);
+  return launch(norm_kernel<FMT, 8, PHASE>, grid, T, cluster, stream, launches, a, o);
+}
+
+template <int FMT, int PHASE>
+cudaError_t gate_launch(const GateArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
+  const int64_t warps = a.rows * ((a.cols / kUnit + 31) / 32);
+  int64_t grid = PHASE == kCluster1 ? kCluster : (warps + 7) / 8;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
+  if (grid > cap) grid = cap;
+  if (PHASE == kOnePass || PHASE == kFormat) {
+    const int64_t pad = (padding_lines(a.rows, a.cols, o) + 255) / 256;
+    if (grid < pad) grid = pad < cap ? pad : cap;
+  }
+  return launch(gate_kernel<FMT, PHASE>, grid, 256, PHASE == kCluster1 ? kCluster : 1, stream, launches, a, o);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
+  const bool units = a.cols % kUnit == 0 && a.cols <= kNormMaxCols &&
+                     fits_units(a.x, a.ld_x) && fits_units(a.weight, 0) &&
+                     (!a.residual || (fits_units(a.residual, a.ld_res) && fits_units(a.residual_out, a.ld_res_out)));
+  switch (o.format) {
+    case NVFP4_OUT_BF16:
+      if (units && fits_units(o.out, o.ld_out)) return norm_launch_u<NVFP4_OUT_BF16, kOnePass>(a, o, launches, stream);
+      return launch(norm_any_kernel, a.rows, 512, 1, stream, launches, a, static_cast<uint16_t*>(o.out), o.ld_out);
+    case NVFP4_OUT_MXFP8: return norm_launch_u<NVFP4_OUT_MXFP8, kOnePass>(a, o, launches, stream);
+    case NVFP4_OUT_MXFP4: return norm_launch_u<NVFP4_OUT_MXFP4, kOnePass>(a, o, launches, stream);
+    default: break;
+  }
+  if (o.gs_in) return norm_launch_u<NVFP4_OUT_NVFP4, kOnePass>(a, o, launches, stream);
+  if (a.rows <= kCluster) return norm_launch_u<NVFP4_OUT_NVFP4, kCluster1>(a, o, launches, stream);
+  cudaError_t e = cudaMemsetAsync(o.amax_word, 0, sizeof(uint32_t), stream);
+  if (e == cudaSuccess) e = norm_launch_u<NVFP4_OUT_NVFP4, kAmax>(a, o, launches, stream);
+  if (e == cudaSuccess) e = norm_launch_u<NVFP4_OUT_NVFP4, kFormat>(a, o, launches, stream);
+  return e;
+}
+
+cudaError_t launch_silu_mul(const GateArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
+  switch (o.format) {
+    case NVFP4_OUT_BF16: {
+      if (a.cols % kUnit == 0 && fits_units(a.gate, a.ld_gate) && fits_units(a.up, a.ld_up) &&
+          fits_units(o.out, o.ld_out))
+        return gate_launch<NVFP4_OUT_BF16, kOnePass>(a, o, launches, stream);
+      int64_t grid = (a.rows * a.cols + 255) / 256;
+      const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
+      if (grid > cap) grid = cap;
+      return launch(gate_any_kernel, grid, 256, 1, stream, launches, a, static_cast<uint16_t*>(o.out), o.ld_out);
+    }
+    case NVFP4_OUT_MXFP8: return gate_launch<NVFP4_OUT_MXFP8, kOnePass>(a, o, launches, stream);
+    case NVFP4_OUT_MXFP4: return gate_launch<NVFP4_OUT_MXFP4, kOnePass>(a, o, launches, stream);
+    default: break;
+  }
+  if (o.gs_in) return gate_launch<NVFP4_OUT_NVFP4, kOnePass>(a, o, launches, stream);
+  // a small output: one cluster computes the amax and formats
+  if (a.rows * a.cols <= 256 * 1024) return gate_launch<NVFP4_OUT_NVFP4, kCluster1>(a, o, launches, stream);
+  cudaError_t e = cudaMemsetAsync(o.amax_word, 0, sizeof(uint32_t), stream);
+  if (e == cudaSuccess) e = gate_launch<NVFP4_OUT_NVFP4, kAmax>(a, o, launches, stream);
+  if (e == cudaSuccess) e = gate_launch<NVFP4_OUT_NVFP4, kFormat>(a, o, launches, stream);
+  return e;
+}
+
+}  // namespace nvfp4
