@@ -351,10 +351,10 @@ nvfp4_status nvfp4_silu_mul(const void *gate, int64_t ld_gate, const void *up, i
  *   gate_codes, gate_scales, gate_global_scale  NULL, or a second N x K weight G:
  *                y = silu(x G^T) * (x W^T), both products unrounded in FP32.
  *   out          device BF16, M x N, row stride ld_out >= N (2-byte aligned, any stride).
- *   0 <= M <= 16, N >= 1, K >= 32, K % 32 == 0.
+ *   0 <= M <= 16, 1 <= N <= 2^30, 32 <= K <= 2^19, K % 32 == 0.
  * FP32 accumulation, no workspace, the same bits on every call.  Weights are exact; x is
- * exact down to 2^-21 of the largest finite magnitude of its token (in the K range that a
- * warp stages at a time), below that rounded at 2^-32 of it.
+ * exact down to 2^-21 of the largest finite magnitude of its token (in the part of K that
+ * a CTA handles), below that rounded at 2^-32 of it.
  * Errors: INVALID_ARG, SHAPE, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA. */
 nvfp4_status nvfp4_matvec(const void *x, const uint8_t *x_scales, nvfp4_sf_layout x_layout, int64_t M, int64_t K,
                           int64_t ld_x, const uint8_t *w_codes, const uint8_t *w_scales,

@@ -44,7 +44,7 @@ def values(x):
 # K: one block pair, partial chunks, fewer chunks than warps, several slices of x
 SHAPES = [(1, 1, 32), (1, 5, 64), (3, 33, 96), (2, 130, 1056), (5, 1001, 160), (8, 256, 2048), (9, 200, 4096),
           (16, 300, 4128), (16, 77, 21504), (1, 14336, 4096), (7, 520, 14336), (11, 96, 28672), (1, 64, 65536),
-          (16, 8192, 512), (13, 20000, 128)]
+          (16, 8192, 512), (13, 20000, 128), (16, 40, 65536), (1, 33, 524288), (12, 30000, 2048), (2, 65536, 64)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

@@ -120,7 +120,7 @@ def test_matvec_validation(lib, mx):
                                 ld_out, None)
 
     assert mv() in NO_DEVICE and mv(M=0) in NO_DEVICE and mv(M=16) in NO_DEVICE
-    assert mv(M=17) == 2 and mv(K=48, ld=48) == 2
+    assert mv(M=17) == 2 and mv(K=48, ld=48) == 2 and mv(K=(1 << 19) + 32, ld=1 << 20) == 2
     assert mv(M=-1) == 1 and mv(N=0) == 1 and mv(K=0) == 1
     assert mv(ld=32) == 1 and mv(ld_out=95) == 1
     assert mv(x=0) == 1 and mv(out=0) == 1 and mv(wc=0) == 1 and mv(wsc=0) == 1

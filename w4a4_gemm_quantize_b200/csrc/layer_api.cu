@@ -111,7 +111,7 @@ nvfp4_status matvec(const void* x, const uint8_t* x_scales, int x_layout, int64_
   nvfp4::g_last_launches = 0;
   if (M < 0 || N < 1 || K < 1 || ld_x < K || ld_out < N) return NVFP4_ERR_INVALID_ARG;
   if (x_scales && x_layout != NVFP4_SF_SWIZZLED && x_layout != NVFP4_SF_LINEAR) return NVFP4_ERR_INVALID_ARG;
-  if (K % 32 != 0 || M > nvfp4::kMatvecMaxTokens || N > INT32_MAX || K > INT32_MAX) return NVFP4_ERR_SHAPE;
+  if (K % 32 != 0 || M > nvfp4::kMatvecMaxTokens || N > kMaxRows || K > (int64_t{1} << 19)) return NVFP4_ERR_SHAPE;
   if (!w.codes || !w.scales || (!mx && !w.gs) || (M > 0 && (!x || !out))) return NVFP4_ERR_INVALID_ARG;
   if ((gate.codes != nullptr) != (gate.scales != nullptr) || (!mx && (gate.codes != nullptr) != (gate.gs != nullptr)))
     return NVFP4_ERR_INVALID_ARG;

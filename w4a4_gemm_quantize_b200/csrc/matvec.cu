@@ -10,20 +10,24 @@
 // [2^-10, 2688], so NVFP4 weights are exact in binary16.  E8M0 scales do not fit
 // binary16; there the mma runs on the bare codes of one block and the binary32 partial
 // product is multiplied by the block's power of two.  x becomes binary16 scaled by a
-// power of two per token and K slice, its largest finite magnitude in [2^7, 2^8): values
-// down to 2^-21 of that largest one keep all their bits, smaller ones are rounded at
-// 2^-32 of it, below the binary32 sum's own rounding.  Sums are binary32 throughout.
+// power of two per token (over the part of K that a CTA handles), its largest finite
+// magnitude in [2^7, 2^8): values down to 2^-21 of that largest one keep all their bits,
+// smaller ones are rounded at 2^-32 of it, below the binary32 sum's own rounding.  Sums
+// are binary32 throughout.
 //
-// Layout: the K axis is cut into chunks of 128 values, dealt round-robin to the CTA's
-// warps; a warp keeps its chunks of x in shared memory as mma fragments and walks down
-// the CTA's weight rows, 16 at a time, each lane loading 16 bytes (32 codes) of two
-// rows.  The mma's k order is free as long as both operands agree, so the fragments are
-// cut to what a lane has loaded: no shuffles for NVFP4, and a 4 x 4 word transpose
-// within the quad for MXFP4 (each mma then stays inside one scale block).  Row order is
-// free too: a tile's 16 rows are 4 neighbours in each of the 4 row quarters of a
-// 128-row group, whose scales lie in 64 contiguous bytes per 4 blocks.  A CTA owns a
-// run of such neighbour lines, so that rows divide over the SMs to within 4.  At the end
-// the warps' partial sums meet in shared memory in a fixed order: no atomics, no
+// Layout.  K is cut into chunks of 256 values (128 where K is no multiple of 64), N into
+// tiles of 16 rows: 4 neighbours in each of the 4 row quarters of a 128-row group, whose
+// scales lie side by side in the 128 x 4 scale tiles (row order is free).  A CTA owns a
+// run of tiles -- all of K, or, where rows are few and long, one part of it in a cluster
+// that shares the tiles -- and puts its part of x into shared memory once, cut into mma
+// fragments.  Its (tile, chunk) items, chunks fastest, are dealt to the warps in equal
+// runs; a warp keeps a tile's sums in registers along the chunks.  Weights come through
+// a ring of asynchronous copies in shared memory, private to the warp, 128 (64)
+// contiguous bytes per row.  The mma's k order is free as long as both operands agree:
+// for NVFP4 a lane takes the codes whose scales are its own, for MXFP4 ldmatrix deals
+// each 16-byte block to a quad, so that an mma stays inside one scale block.  A tile that
+// ends in another warp's run leaves its sums in a slot per warp; the slots meet in a fixed
+// order (a cluster's through distributed shared memory): no atomics on sums, no
 // workspace, the same bits on every call.
 #include <cuda_runtime.h>
 
@@ -34,30 +38,48 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kChunk = 128;      // K values of one warp step
-constexpr int kMaxWarps = 16;
-constexpr int kDepth = 4;        // weight steps in flight per warp
+constexpr int kWarps = 16, kThreads = kWarps * 32;
+constexpr int kDepth = 2;        // weight items in flight per warp (3 and 4: no faster, less room for x)
 constexpr int kPad = 20;         // floats per token of a 16-row partial (padded: conflict-free)
-constexpr int kMaxSlice = 12;    // chunks of x a warp holds at a time, at most
-constexpr int kXBytes = 10240;   // shared memory for them, per warp
-constexpr int kSmem = 220 * 1024;
+constexpr int kUnit = 256;       // K is divided in units of this between a cluster's CTAs
+constexpr int kSmem = 226 * 1024;
 
 struct Params {
   MatvecArgs a;
-  int64_t lines;      // 4-row neighbour lines of the weight
-  int chunks;         // ceil(K / 128)
-  int slice;          // chunks of x per warp and slice
-  int batch;          // row tiles between two reductions
-  int64_t atoms;      // scale atoms (4 blocks) per 128-row group
-  uint32_t last_mask; // MXFP4: the scale bytes of the last chunk that are blocks of the row
+  int tiles;          // of 16 rows (gated: 8 of each weight)
+  int units;          // of 256 K values
+  int atoms;          // scale atoms (4 blocks) per 128-row group
+  int batch;          // tiles between two reductions
+  int split;          // CTAs of a cluster that share tiles, each a part of K
+  int x_units;        // units of a part, at most
+  uint32_t m_inv;     // ceil(2^32 / M): x / M = mulhi(x, m_inv) for the small x it is used on
+  int tiles_q, tiles_r, units_q, units_r;  // tiles per CTA (cluster) and units per part, and remainders
 };
 
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// First of `items` that warp w handles (w = kWarps: the end): equal runs, none empty before
+// a warp that has one.
+__device__ __forceinline__ int run_start(int items, int w) {
+  return items < kWarps ? min(w, items) : items * w / kWarps;
+}
+
+__device__ __forceinline__ int div_m(const Params& p, int x) {
+  return p.a.M == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), p.m_inv));
+}
+
+// Asynchronous 16-byte copies, global to shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // the eight E2M1 codes of a word as four binary16 pairs, element 2i in the low half
@@ -113,325 +135,553 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// w[b] of lane t <- w[t] of lane b, within each quad of lanes
-__device__ __forceinline__ void transpose_quad(uint32_t (&w)[4], int t) {
-  const bool odd = t & 1, high = t & 2;
+// eight E4M3 codes times their scale
+__device__ __forceinline__ void fp8_values(uint32_t lo4, uint32_t hi4, float s, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const uint32_t r = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[i] : w[i + 1], 1);
-    (odd ? w[i] : w[i + 1]) = r;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t r = __shfl_xor_sync(0xFFFFFFFFu, high ? w[i] : w[i + 2], 2);
-    (high ? w[i] : w[i + 2]) = r;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = e4m3x2_to_half2(((i < 2 ? lo4 : hi4) >> (16 * (i & 1))) & 0xFFFFu);
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}\n"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+    v[2 * i] = lo * s;
+    v[2 * i + 1] = hi * s;
   }
 }
 
-// Eight consecutive values of x: BF16 (16 bytes) or E4M3 with their scale byte.
-struct Piece {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   uint4 v;
-  uint32_t scale;
-};
-
-__device__ __forceinline__ Piece load_piece(const MatvecArgs& a, int m, int64_t k) {
-  Piece p{make_uint4(0u, 0u, 0u, 0u), 127u};
-  if (k >= a.K) return p;
-  if (a.x_scales == nullptr) {
-    p.v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ld_x + k));
-  } else {
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + m * a.ld_x + k));
-    p.v.x = c.x;
-    p.v.y = c.y;
-    const int64_t b = k >> 5;
-    p.scale = __ldg(a.x_scales + (a.x_swizzled ? (b >> 2) * 512 + m * 16 + (b & 3) : m * (a.K >> 5) + b));
-  }
-  return p;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
 
-__device__ __forceinline__ void piece_values(const Piece& p, bool fp8, float (&v)[8]) {
-  if (!fp8) {
-    const uint32_t w[4] = {p.v.x, p.v.y, p.v.z, p.v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    float s, unused;
-    e8m0x2_to_float(p.scale, s, unused);
-    const uint32_t w[2] = {p.v.x, p.v.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t h = e4m3x2_to_half2((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-      float lo, hi;
-      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}\n"
-          : "=f"(lo), "=f"(hi)
-          : "r"(h));
-      v[2 * i] = lo * s;
-      v[2 * i + 1] = hi * s;
-    }
-  }
+// Four 8 x 16-byte matrices of shared memory (lane l: the address of row l & 7 of matrix
+// l >> 3): register i holds word t of row g of matrix i.
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
 }
 
-// Puts x's chunks first, first + W, ... (n of them) of every token into the warp's shared
-// memory as scaled binary16 mma fragments: 16 bytes for (chunk, word j, token, lane t)
-// hold the 8 values from k = 32 t + 8 j (NVFP4) or 32 j + 8 t (MXFP4) of the chunk.
-// mult[m] = the power of two that undoes token m's scaling.
-template <bool MX>
-__device__ __noinline__ void stage_x(const Params& p, int first, int W, int n, uint4* xs, float* mult) {
-  const int lane = threadIdx.x & 31;
-  const bool fp8 = p.a.x_scales != nullptr;
-  const int M = p.a.M, pieces = n * 16;
-  for (int m = 0; m < M; ++m) {
-    Piece q[kMaxSlice / 2];
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxSlice / 2; ++i) {
-      const int id = lane + 32 * i;
-      if (id >= pieces) break;
-      const int64_t k = static_cast<int64_t>(first + (id >> 4) * W) * kChunk + (id & 15) * 8;
-      q[i] = load_piece(p.a, m, k);
-    }
-#pragma unroll
-    for (int i = 0; i < kMaxSlice / 2; ++i) {
-      if (lane + 32 * i >= pieces) break;
-      float v[8];
-      piece_values(q[i], fp8, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-        top = max(top, b < 0x7F800000u ? b : 0u);  // infinities and NaN keep to themselves
+// Power of two 2^e, e a binary32 exponent
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// The exponent E by which a token's values are scaled down, from the bits of its largest
+// finite magnitude: 2^-E brings it into [2^7, 2^8) (tiny ones as near as binary32 allows).
+__device__ __forceinline__ int down_exponent(uint32_t top) {
+  return top == 0u ? 0 : max(-126, static_cast<int>(top >> 23) - 127 - 7);
+}
+
+// x in shared memory.  The part from unit u0 on (n units) of every token becomes scaled
+// binary16 mma fragments: 512 bytes per (unit, token), in which place (j, t) of 16 bytes
+// holds the 8 values that lane t of a quad multiplies with its word j of the unit's codes.
+// Odd tokens have the places of each pair j, j + 1 exchanged, so that two tokens' quads
+// read 8 different bank groups.  One warp per (unit, token), a lane per piece of 8 values.
+// fetch() copies the pieces as they come (E4M3: 8 bytes, then the word that holds their
+// scale), ahead of the weight stream; stage() scales them and puts them in place.  (Copying
+// straight to the places, whose stride is 64 bytes or more, took 600 cycles a copy.)
+// Rolled loops: the code runs once per launch, from a cold instruction cache.
+template <bool MX, int WORDS>
+struct Stager {
+  const Params& p;
+  const int u0, pairs;
+  uint4* const xs;
+
+  // Calls f(pair, unit, token) for the warp's pairs.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int M = p.a.M, step_u = div_m(p, kWarps), step_m = kWarps - step_u * M;
+    int pair = threadIdx.x >> 5, u = div_m(p, pair), m = pair - u * M;
+#pragma unroll 1
+    for (; pair < pairs; pair += kWarps) {
+      f(pair, u, m);
+      u += step_u;
+      m += step_m;
+      if (m >= M) {
+        m -= M;
+        ++u;
       }
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    // the largest magnitude 2^e.. goes to [2^7, 2^8); E stays a binary32 exponent
-    const int E = top == 0u ? 0 : max(-126, static_cast<int>(top >> 23) - 127 - 7);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
-    if (lane == 0) mult[m] = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
-#pragma unroll
-    for (int i = 0; i < kMaxSlice / 2; ++i) {
-      const int id = lane + 32 * i;
-      if (id >= pieces) break;
-      float v[8];
-      piece_values(q[i], fp8, v);
-      uint4 h;
-      h.x = pack_half(v[0] * down, v[1] * down);
-      h.y = pack_half(v[2] * down, v[3] * down);
-      h.z = pack_half(v[4] * down, v[5] * down);
-      h.w = pack_half(v[6] * down, v[7] * down);
-      const int c = id >> 4, o = id & 15;
-      const int j = MX ? o >> 2 : o & 3, t = MX ? o & 3 : o >> 2;
-      xs[((c * 4 + j) * M + m) * 4 + t] = h;
-    }
   }
-}
+  __device__ __forceinline__ uint4* raw(int pair) const { return xs + pair * 32 + (threadIdx.x & 31); }
+  __device__ __forceinline__ int k_of(int u) const { return (u0 + u) * kUnit + (threadIdx.x & 31) * 8; }
+  __device__ __forceinline__ int scale_of(int m, int k) const {
+    const int b = k >> 5;
+    return p.a.x_swizzled ? (b >> 2) * 512 + m * 16 + (b & 3) : m * static_cast<int>(p.a.K >> 5) + b;
+  }
 
-// 128 K values of a lane's two weight rows: 32 codes each, and their scales (NVFP4: the
-// two bytes of the lane's blocks; MXFP4: the four bytes of the chunk's blocks).
-struct Step {
-  uint4 a, b;
-  uint32_t sa, sb;
+  __device__ __forceinline__ void fetch() const {
+    const MatvecArgs& a = p.a;
+    each([&](int pair, int u, int m) {
+      const int k = k_of(u);
+      const uint32_t dst = smem_u32(raw(pair));
+      if (k >= a.K) {
+        st_shared16(dst, make_uint4(0u, 0u, a.x_scales ? 0x7F7F7F7Fu : 0u, 0u));
+      } else if (a.x_scales == nullptr) {
+        copy16(dst, static_cast<const uint8_t*>(a.x) + (m * a.ld_x + k) * 2);
+      } else {
+        copy8(dst, static_cast<const uint8_t*>(a.x) + m * a.ld_x + k);
+        const int at = scale_of(m, k), word = at & ~3;
+        if (a.x_swizzled || word + 4 <= a.M * static_cast<int>(a.K >> 5))
+          copy4(dst + 8, a.x_scales + word);
+        else  // the last bytes of a linear buffer that ends inside a word
+          st_shared4(dst + 8, static_cast<uint32_t>(__ldg(a.x_scales + at)) * 0x01010101u);
+      }
+    });
+    copies_commit();
+  }
+
+  // the values of an MXFP8 piece
+  __device__ __forceinline__ void fp8(uint4 v, int u, int m, float (&f)[8]) const {
+    float s, unused;
+    e8m0x2_to_float((v.z >> (8 * (scale_of(m, k_of(u)) & 3))) & 0xFFu, s, unused);
+    fp8_values(v.x, v.y, s, f);
+  }
+
+  // top: a zeroed word per token, receives the bits of its largest finite magnitude, whose
+  // down_exponent the scaling is.  Every lane reads the pieces it copied.
+  __device__ __forceinline__ void stage(uint32_t* top) const {
+    const bool mx8 = p.a.x_scales != nullptr;
+    each([&](int pair, int u, int m) {
+      const uint4 v = *raw(pair);
+      uint32_t big = 0;
+      if (mx8) {
+        float f[8];
+        fp8(v, u, m, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+          big = max(big, b < 0x7F800000u ? b : 0u);  // infinities and NaN do not set the scale
+        }
+      } else {
+        const uint32_t k = 0x7FFF7FFFu;
+        const uint32_t two = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+        big = max(two & 0xFFFFu, two >> 16);
+        if (big >= 0x7F80u) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          big = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t b = (w[e >> 1] >> (16 * (e & 1))) & 0x7FFFu;
+            big = max(big, b < 0x7F80u ? b : 0u);
+          }
+        }
+        big <<= 16;
+      }
+      big = __reduce_max_sync(0xFFFFFFFFu, big);
+      if ((threadIdx.x & 31) == 0) atomicMax(top + m, big);
+    });
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const int j = MX ? lane >> 2 : WORDS == 8 ? lane & 7 : (lane >> 4) * 4 + (lane & 3);
+    const int t = MX ? lane & 3 : WORDS == 8 ? lane >> 3 : (lane >> 2) & 3;
+    const uint32_t place = smem_u32(xs + j * 4 + t);
+    each([&](int pair, int u, int m) {
+      const uint4 v = *raw(pair);
+      const float down = exp2_int(-down_exponent(top[m]));
+      __syncwarp();  // the pair's pieces have been read: its 512 bytes may be written
+      float f[8];
+      if (mx8) {
+        fp8(v, u, m, f);
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = __uint_as_float(w[i] << 16);
+          f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
+      st_shared16((place + pair * 512) ^ ((m & 1) << 6),
+                  make_uint4(pack_half(f[0] * down, f[1] * down), pack_half(f[2] * down, f[3] * down),
+                             pack_half(f[4] * down, f[5] * down), pack_half(f[6] * down, f[7] * down)));
+    });
+  }
 };
 
-template <bool MX, int NT, bool GATED>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec_kernel(const Params p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float mults[kMaxWarps][kMatvecMaxTokens];
+// One item in a warp's ring: 16 R rows of codes (the 16-byte pieces of a row permuted so that
+// every access below is free of bank conflicts), then its scale lines, 4 R per atom.
+template <bool MX, int WORDS, int R>
+struct ItemBytes {
+  static constexpr int kRow = WORDS * 16;                   // bytes of codes per row
+  static constexpr int kAtoms = WORDS / (MX ? 4 : 2);       // scale atoms
+  static constexpr int kScales = 16 * R * kRow;             // where the scales begin
+  static constexpr int kBytes = kScales + 64 * R * kAtoms;
+  __device__ static int place(int m, int piece) {
+    return m * kRow + ((piece ^ (WORDS == 8 ? m & 7 : (m >> 1) & 3)) << 4);
+  }
+};
+
+// WORDS: 32-bit words of codes per lane and row of an item: 8 (chunks of 256) or 4 (128).
+// R: 16-row groups of a tile (2 only with WORDS 4: each word of x then serves two of them).
+template <bool MX, int NT, bool GATED, int WORDS, int R>
+__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using Ring = ItemBytes<MX, WORDS, R>;
+  constexpr int kPerUnit = 8 / WORDS;              // chunks per unit
+  constexpr int kLines = (GATED ? 2 : 4) * R;      // neighbour lines of a tile
+  constexpr int kCopies = WORDS / 2 * R;           // copies per lane for the codes
+  static_assert(WORDS == 4 || R == 1, "a 256-value chunk of one 16-row group, or 128 of one or two");
+  constexpr int W = kWarps;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int M = p.a.M, slot = M * kPad * R;
+  const uint32_t ring = smem_u32(smem) + warp * kDepth * Ring::kBytes;
+  uint4* xs = reinterpret_cast<uint4*>(smem + W * kDepth * Ring::kBytes);
+  uint32_t* top = reinterpret_cast<uint32_t*>(xs + p.x_units * M * 32);  // per token: largest magnitude
+  uint8_t* first = reinterpret_cast<uint8_t*>(top + kMatvecMaxTokens);   // per tile: first and last warp
+  uint8_t* last = first + p.batch;
+  float* part = reinterpret_cast<float*>(first + (2 * p.batch + 15) / 16 * 16);  // slot of (tile, warp): tile + warp
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int group = p.split > 1 ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int T0 = group * p.tiles_q + min(group, p.tiles_r), T1 = T0 + p.tiles_q + (group < p.tiles_r);
+  const int u0 = rank * p.units_q + min(rank, p.units_r), un = p.units_q + (rank < p.units_r);
+  const int row_bytes = static_cast<int>(p.a.K / 2);
+  const int chunk0 = u0 * kPerUnit;
+  // chunks of this part (the last unit may end inside its first chunk of 128), those whole
+  const int chunks = min(un * kPerUnit, (row_bytes + Ring::kRow - 1) / Ring::kRow - chunk0);
+  const int whole = min(chunks, row_bytes / Ring::kRow - chunk0);
+  const int64_t group_bytes = static_cast<int64_t>(p.atoms) * 512;
+  const int N = static_cast<int>(p.a.N);
+  if (threadIdx.x < kMatvecMaxTokens) top[threadIdx.x] = 0u;
+
+  // Load side: walks the items of this warp, batch after batch, kDepth ahead of the other.
+  // A lane copies 16-byte pieces of row quarter lq, with WORDS 8 of one row per copy, with
+  // WORDS 4 of two.
+  const int lq = WORDS == 8 ? lane >> 3 : (lane >> 2) & 3;
+  const int lpiece = WORDS == 8 ? lane & 7 : lane & 3;
+  const int lline = WORDS == 8 ? 0 : lane >> 4;  // line of the first copy
+  const uint32_t ldst = ring + (WORDS == 8 ? Ring::place(lq, lpiece) : Ring::place(lane >> 2, lpiece));
+  const uint32_t sdst = ring + Ring::kScales + lane * 16;
+  const int64_t lane_off = (32 * lq + lline) * static_cast<int64_t>(row_bytes) + lpiece * 16;
+  const uint8_t* const codes0 = (GATED ? p.a.gate.codes : p.a.w.codes) + lane_off;
+  const int64_t gate_to_w = GATED ? static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.a.w.codes) -
+                                                         reinterpret_cast<uintptr_t>(p.a.gate.codes))
+                                  : 0;
+  // a lane per 16-byte scale line, 4 R lines of each atom: rows 4 line .. of the tile
+  const bool scale_lane = lane < 4 * R * Ring::kAtoms;
+  const int satom = lane / (4 * R), sline = lane % (4 * R);
+  const uint8_t* const scales0 = (GATED && (sline & 2) == 0 ? p.a.gate.scales : p.a.w.scales) + satom * 512 +
+                                 (GATED ? (sline >> 2) * 2 + (sline & 1) : sline) * 16;
+  // Segments: consecutive chunks of one tile.
+  int ltile = T0, lt = 0, lc = 0, left = 0;  // batch: first tile; next tile and chunk; items left
+  int run = 0;                               // items left of the segment
+  bool full = false;                         // every row and byte of its items is inside the weight
+  int rows = 0, lchunk = 0;                  // otherwise: rows of this lane's quarter, the chunk
+  const uint8_t *pc = codes0, *ps = scales0;
+  auto segment = [&]() {
+    while (left == 0 && ltile < T1) {
+      const int nt = min(p.batch, T1 - ltile), items = nt * chunks, i0 = run_start(items, warp);
+      left = run_start(items, warp + 1) - i0;
+      lt = i0 / chunks;
+      lc = i0 - lt * chunks;
+      if (left == 0) ltile += nt;  // (fewer items than warps)
+    }
+    if (left == 0) return;
+    const int line = (ltile + lt) * kLines;
+    const int row0 = (line >> 5) * 128 + (line & 31);
+    lchunk = chunk0 + lc;
+    pc = codes0 + static_cast<int64_t>(row0) * row_bytes + lchunk * Ring::kRow;
+    ps = scales0 + (line >> 5) * group_bytes + (line & 31) * 16 + lchunk * static_cast<int64_t>(Ring::kAtoms * 512);
+    full = (line >> 5) * 128 + 128 <= N && lc < whole;
+    rows = N - row0 - 32 * lq - lline;
+    run = full ? min(left, whole - lc) : 1;
+    left -= run;
+    lc += run;
+    if (lc == chunks) {
+      lc = 0;
+      ++lt;
+    }
+    if (left == 0) ltile += min(p.batch, T1 - ltile);
+  };
+  auto load = [&](int at) {  // at: the slot's offset in the ring
+    if (run == 0) segment();
+    if (run > 0) {
+      const uint8_t* pw = pc + gate_to_w;
+      const uint32_t d0 = ldst + at, d1 = (ldst ^ 64u) + at;
+      if (full) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          // line of the copy (less lline): rows 4 line .. of the tile, the gate's before w's in each 16
+          const int l = WORDS == 8 ? (GATED ? i & 1 : i) : (GATED ? i & ~1 : 2 * i);
+          const bool of_w = GATED && (WORDS == 8 ? i >= 2 : i & 1);
+          copy16((WORDS == 8 && (i & 1) ? d1 : d0) + i * 512,
+                 (of_w ? pw : pc) + static_cast<uint64_t>(static_cast<uint32_t>(row_bytes)) * l);
+        }
+        if (scale_lane) copy16(sdst + at, ps);
+      } else {
+        // a row or piece outside the weight keeps what the ring held: the row's sums are never
+        // written, the piece meets zeros of x
+        const bool in = lchunk * Ring::kRow + lpiece * 16 < row_bytes;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int l = WORDS == 8 ? (GATED ? i & 1 : i) : (GATED ? i & ~1 : 2 * i);
+          const bool of_w = GATED && (WORDS == 8 ? i >= 2 : i & 1);
+          if (in && l < rows)
+            copy16((WORDS == 8 && (i & 1) ? d1 : d0) + i * 512,
+                   (of_w ? pw : pc) + static_cast<int64_t>(row_bytes) * l);
+        }
+        // scales past the row's end are cleared, whatever the padding holds: zero by zero
+        const int blocks = row_bytes / (MX ? 16 : 8) - 4 * (lchunk * Ring::kAtoms + satom);
+        if (scale_lane) {
+          if (blocks >= 4) {
+            copy16(sdst + at, ps);
+          } else {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (blocks > 0) {
+              const uint32_t mask = (1u << (8 * blocks)) - 1u;
+              v = __ldg(reinterpret_cast<const uint4*>(ps));
+              v = make_uint4(v.x & mask, v.y & mask, v.z & mask, v.w & mask);
+            }
+            st_shared16(sdst + at, v);
+          }
+        }
+      }
+      pc += Ring::kRow;
+      ps += Ring::kAtoms * 512;
+      --run;
+    }
+    copies_commit();  // (empty past the end: the wait counts groups)
+  };
+  if (p.split > 1) cluster_arrive();  // waited for before the first store into another CTA
+  __syncthreads();                    // `top` is zeroed
+  segment();
   grid_dependency_wait();
   grid_dependents_launch();
-  constexpr int kLines = GATED ? 2 : 4;  // neighbour lines of a 16-row tile
-  const int W = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int M = p.a.M;
-  uint4* xs = reinterpret_cast<uint4*>(smem) + static_cast<size_t>(warp) * p.slice * M * 16;
-  float* part = reinterpret_cast<float*>(smem + static_cast<size_t>(W) * p.slice * M * 256);
-  float* mult = mults[warp];
-  const int64_t l0 = p.lines * blockIdx.x / gridDim.x, l1 = p.lines * (blockIdx.x + 1) / gridDim.x;
-  const int tiles = static_cast<int>((l1 - l0 + kLines - 1) / kLines);
-  const int mine = p.chunks > warp ? (p.chunks - warp + W - 1) / W : 0;  // chunks of this warp
-  const int64_t row_bytes = p.a.K / 2;
+  const Stager<MX, WORDS> stager{p, u0, un * M, xs};
+  stager.fetch();
+#pragma unroll 1
+  for (int d = 0; d < kDepth; ++d) load(d * Ring::kBytes);
+  copies_wait<kDepth>();  // x, not yet the weights
+  stager.stage(top);
+  __syncthreads();
 
-  for (int tile0 = 0; tile0 < tiles; tile0 += p.batch) {
-    const int nt = min(p.batch, tiles - tile0);
-    if (mine > 0) {
-      // the load side of the pipeline runs kDepth steps ahead of the compute side, both
-      // through slices (outermost), tiles, chunks
-      int ls = 0, lt = 0, lj = 0;  // first chunk of the slice, tile, chunk
-      const uint8_t *pa = nullptr, *pb = nullptr, *sa = nullptr, *sb = nullptr;
-      bool va = false, vb = false, more = true;
-      auto rows_of_tile = [&]() {
-        const int64_t line = l0 + static_cast<int64_t>(tile0 + lt) * kLines + (g >> 2);
-        const int64_t lb = GATED ? line : line + 2;
-        const int64_t ra = (line >> 5) * 128 + (line & 31) + 32 * (g & 3);
-        const int64_t rb = (lb >> 5) * 128 + (lb & 31) + 32 * (g & 3);
-        va = line < l1 && ra < p.a.N;
-        vb = lb < l1 && rb < p.a.N;
-        const Weight4& wa = GATED ? p.a.gate : p.a.w;
-        pa = wa.codes + ra * row_bytes + t * 16;
-        pb = p.a.w.codes + rb * row_bytes + t * 16;
-        const int lane_off = (MX ? 0 : (t >> 1) * 512 + (t & 1) * 2) + (g & 3) * 4;
-        sa = wa.scales + (line >> 5) * p.atoms * 512 + (line & 31) * 16 + lane_off;
-        sb = p.a.w.scales + (lb >> 5) * p.atoms * 512 + (lb & 31) * 16 + lane_off;
-      };
-      rows_of_tile();
-      auto load = [&](Step& s) {
-        s.a = s.b = make_uint4(0u, 0u, 0u, 0u);
-        s.sa = s.sb = 0u;
-        if (!more) return;
-        const int c = warp + (ls + lj) * W;
-        const bool in = c * static_cast<int64_t>(kChunk) + 32 * t < p.a.K;
-        const int64_t co = static_cast<int64_t>(c) * (kChunk / 2);
-        const int64_t so = static_cast<int64_t>(c) * (MX ? 512 : 1024);
-        if (va && in) s.a = ld_stream(pa + co);
-        if (vb && in) s.b = ld_stream(pb + co);
-        if constexpr (MX) {
-          if (va) s.sa = __ldg(reinterpret_cast<const uint32_t*>(sa + so));
-          if (vb) s.sb = __ldg(reinterpret_cast<const uint32_t*>(sb + so));
-          if (c == p.chunks - 1) {  // the padding's bytes, whatever they hold, scale zero codes
-            s.sa &= p.last_mask;
-            s.sb &= p.last_mask;
-          }
-        } else {
-          if (va && in) s.sa = __ldg(reinterpret_cast<const uint16_t*>(sa + so));
-          if (vb && in) s.sb = __ldg(reinterpret_cast<const uint16_t*>(sb + so));
-        }
-        if (++lj == min(p.slice, mine - ls)) {
-          lj = 0;
-          if (++lt == nt) {
-            lt = 0;
-            ls += p.slice;
-            more = ls < mine;
-          }
-          if (more) rows_of_tile();
-        }
-      };
-      Step ring[kDepth];
+  // Compute side: a lane's places in a slot of the ring and in x (a token that is not there
+  // repeats the last one: its sums are not kept).
+  const uint32_t codes_at = ring + (MX ? Ring::place((lane & 7) + (lane & 8), lane >> 4) : Ring::place(g, t * (WORDS / 4)));
+  const uint32_t scales_at = ring + Ring::kScales + g * 4 + (MX ? 0 : (WORDS == 8 ? t : t >> 1) * 64 * R);
+  uint32_t x_at[NT], x_flip[NT];  // of word 0 of the part; 64 for odd tokens
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) load(ring[d]);
-
-      int cs = 0, ct = 0, cj = 0;
-      float acc[NT][4];
+  for (int n = 0; n < NT; ++n) {
+    const int m = min(g + 8 * n, M - 1);
+    x_at[n] = smem_u32(xs + m * 32 + t);
+    x_flip[n] = (m & 1) * 64;
+  }
+  int at = 0;  // the slot's offset in the ring
+  for (int tile0 = T0; tile0 < T1; tile0 += p.batch) {
+    const int nt = min(p.batch, T1 - tile0);
+    const int items = nt * chunks;
+    const int i0 = run_start(items, warp);
+    int todo = run_start(items, warp + 1) - i0;
+    int ti = i0 / chunks, c = i0 - ti * chunks;
+    while (todo > 0) {
+      const int stop = min(chunks, c + todo);
+      todo -= stop - c;
+      if (lane == 0) {
+        if (c == 0) first[ti] = static_cast<uint8_t>(warp);
+        if (stop == chunks) last[ti] = static_cast<uint8_t>(warp);
+      }
+      float acc[R][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-      bool done = false;
-      while (!done) {
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-          if (done) break;
-          if (cj == 0 && ct == 0) {  // a new slice of x
-            __syncwarp();            // every lane is through with the last one
-            stage_x<MX>(p, warp + cs * W, W, min(p.slice, mine - cs), xs, mult);
-            __syncwarp();
-          }
-          Step& s = ring[d];
-          uint32_t wa[4] = {s.a.x, s.a.y, s.a.z, s.a.w}, wb[4] = {s.b.x, s.b.y, s.b.z, s.b.w};
-          uint32_t ha2[2], hb2[2];
-          float fa[4], fb[4];
+        for (int n = 0; n < NT; ++n) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.0f;
+#pragma unroll 1
+      for (; c < stop; ++c) {
+        copies_wait<kDepth - 1>();
+        __syncwarp();  // every lane's copies of this item have landed
+        uint32_t wa[R][WORDS], wb[R][WORDS];
+        uint32_t ha[R][WORDS / 2], hb[R][WORDS / 2];  // NVFP4: block scales, twice each
+        float fa[R][WORDS], fb[R][WORDS];             // MXFP4: block scales
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t src = codes_at + at + r * 16 * Ring::kRow, ssrc = scales_at + at + r * 64;
           if constexpr (MX) {
-            transpose_quad(wa, t);
-            transpose_quad(wb, t);
-            e8m0x2_to_float(s.sa & 0xFFFFu, fa[0], fa[1]);
-            e8m0x2_to_float(s.sa >> 16, fa[2], fa[3]);
-            e8m0x2_to_float(s.sb & 0xFFFFu, fb[0], fb[1]);
-            e8m0x2_to_float(s.sb >> 16, fb[2], fb[3]);
-          } else {
-            const uint32_t a2 = e4m3x2_to_half2(s.sa), b2 = e4m3x2_to_half2(s.sb);
-            ha2[0] = __byte_perm(a2, 0u, 0x1010), ha2[1] = __byte_perm(a2, 0u, 0x3232);
-            hb2[0] = __byte_perm(b2, 0u, 0x1010), hb2[1] = __byte_perm(b2, 0u, 0x3232);
-          }
-          load(s);  // the slot is free
+            // word j: lane t's word of the chunk's block j
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < WORDS; j += 2) ldmatrix4(src ^ (j << 4), wa[r][j], wb[r][j], wa[r][j + 1], wb[r][j + 1]);
+#pragma unroll
+            for (int h = 0; h < WORDS / 4; ++h) {
+              const uint32_t sa = ld_shared4(ssrc + 64 * R * h), sb = ld_shared4(ssrc + 64 * R * h + 32);
+              e8m0x2_to_float(sa & 0xFFFFu, fa[r][4 * h], fa[r][4 * h + 1]);
+              e8m0x2_to_float(sa >> 16, fa[r][4 * h + 2], fa[r][4 * h + 3]);
+              e8m0x2_to_float(sb & 0xFFFFu, fb[r][4 * h], fb[r][4 * h + 1]);
+              e8m0x2_to_float(sb >> 16, fb[r][4 * h + 2], fb[r][4 * h + 3]);
+            }
+          } else {
+            // word j: codes 8 j .. of the lane's own 32 (16) bytes of the row
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+              const uint4 a = ld_shared16(src ^ (i << 4));
+              const uint4 b = ld_shared16((src ^ (i << 4)) + 8 * Ring::kRow);
+              wa[r][4 * i] = a.x, wa[r][4 * i + 1] = a.y, wa[r][4 * i + 2] = a.z, wa[r][4 * i + 3] = a.w;
+              wb[r][4 * i] = b.x, wb[r][4 * i + 1] = b.y, wb[r][4 * i + 2] = b.z, wb[r][4 * i + 3] = b.w;
+            }
+            uint32_t sa = ld_shared4(ssrc), sb = ld_shared4(ssrc + 32);
+            if constexpr (WORDS == 4) {
+              sa >>= 16 * (t & 1);
+              sb >>= 16 * (t & 1);
+            }
+#pragma unroll
+            for (int h = 0; h < WORDS / 4; ++h) {
+              const uint32_t a2 = e4m3x2_to_half2((sa >> (16 * h)) & 0xFFFFu);
+              const uint32_t b2 = e4m3x2_to_half2((sb >> (16 * h)) & 0xFFFFu);
+              ha[r][2 * h] = __byte_perm(a2, 0u, 0x1010), ha[r][2 * h + 1] = __byte_perm(a2, 0u, 0x3232);
+              hb[r][2 * h] = __byte_perm(b2, 0u, 0x1010), hb[r][2 * h + 1] = __byte_perm(b2, 0u, 0x3232);
+            }
+          }
+        }
+        __syncwarp();  // the slot has been read by every lane
+        load(at);
+        at = at == (kDepth - 1) * Ring::kBytes ? 0 : at + Ring::kBytes;
+        const uint32_t xc = (c / kPerUnit) * M * 512 + (c % kPerUnit) * (WORDS * 64);
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) {
+          uint4 x[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            x[n] = ld_shared16(x_at[n] + xc + (j & 1 ? 0u - x_flip[n] : x_flip[n]) + j * 64);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
             uint32_t a[4], b[4];
-            codes_to_half(wa[j], a);
-            codes_to_half(wb[j], b);
+            codes_to_half(wa[r][j], a);
+            codes_to_half(wb[r][j], b);
             if constexpr (!MX) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                a[i] = mul_half2(a[i], ha2[j >> 1]);
-                b[i] = mul_half2(b[i], hb2[j >> 1]);
+                a[i] = mul_half2(a[i], ha[r][j >> 1]);
+                b[i] = mul_half2(b[i], hb[r][j >> 1]);
               }
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const int m = g + 8 * n;
-              uint4 x = make_uint4(0u, 0u, 0u, 0u);
-              if (m < M) x = xs[((cj * 4 + j) * M + m) * 4 + t];
+              float(&d)[4] = acc[r][n];
               if constexpr (MX) {
                 float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma(q, a[0], b[0], a[1], b[1], x.x, x.y);
-                mma(q, a[2], b[2], a[3], b[3], x.z, x.w);
-                acc[n][0] = __fmaf_rn(q[0], fa[j], acc[n][0]);
-                acc[n][1] = __fmaf_rn(q[1], fa[j], acc[n][1]);
-                acc[n][2] = __fmaf_rn(q[2], fb[j], acc[n][2]);
-                acc[n][3] = __fmaf_rn(q[3], fb[j], acc[n][3]);
+                mma(q, a[0], b[0], a[1], b[1], x[n].x, x[n].y);
+                mma(q, a[2], b[2], a[3], b[3], x[n].z, x[n].w);
+                d[0] = __fmaf_rn(q[0], fa[r][j], d[0]);
+                d[1] = __fmaf_rn(q[1], fa[r][j], d[1]);
+                d[2] = __fmaf_rn(q[2], fb[r][j], d[2]);
+                d[3] = __fmaf_rn(q[3], fb[r][j], d[3]);
               } else {
-                mma(acc[n], a[0], b[0], a[1], b[1], x.x, x.y);
-                mma(acc[n], a[2], b[2], a[3], b[3], x.z, x.w);
+                mma(d, a[0], b[0], a[1], b[1], x[n].x, x[n].y);
+                mma(d, a[2], b[2], a[3], b[3], x[n].z, x[n].w);
               }
-            }
-          }
-          if (++cj == min(p.slice, mine - cs)) {  // the tile's share of this slice
-            cj = 0;
-            float* out = part + static_cast<size_t>(ct * W + warp) * M * kPad;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int m = 8 * n + 2 * t + (i & 1);
-                if (m < M) {
-                  float* q = out + m * kPad + g + 8 * (i >> 1);
-                  const float v = acc[n][i] * mult[m];
-                  *q = cs == 0 ? v : *q + v;
-                }
-                acc[n][i] = 0.0f;
-              }
-            }
-            if (++ct == nt) {
-              ct = 0;
-              cs += p.slice;
-              done = cs >= mine;
             }
           }
         }
       }
+      float* out = part + (ti + warp) * slot + g;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int m = 8 * n + 2 * t + (i & 1);
+            if (m < M) out[(r * M + m) * kPad + 8 * (i >> 1)] = acc[r][n][i];
+          }
+      c = 0;
+      ++ti;
     }
     __syncthreads();
-    constexpr int kRows = GATED ? 8 : 16;  // outputs of a tile per token
+    constexpr int kRows = GATED ? 8 : 16;  // outputs of a 16-row group per token
     const float sw = p.a.w.gs ? *p.a.w.gs : 1.0f, sgate = GATED && p.a.gate.gs ? *p.a.gate.gs : 1.0f;
-    for (int i = threadIdx.x; i < nt * kRows * M; i += blockDim.x) {
-      const int r = i % kRows, m = (i / kRows) % M, ti = i / (kRows * M);
-      const float* q = part + static_cast<size_t>(ti) * W * M * kPad + m * kPad + r;
-      float s = 0.0f, u = 0.0f;
-      for (int w = 0; w < W; ++w) {
-        s += q[w * M * kPad];
-        if (GATED) u += q[w * M * kPad + 8];
-      }
-      const int64_t line = l0 + static_cast<int64_t>(tile0 + ti) * kLines + (r >> 2);
-      const int64_t row = (line >> 5) * 128 + (line & 31) + 32 * (r & 3);
-      if (line >= l1 || row >= p.a.N) continue;
-      float y;
+    auto write = [&](int i, float s, float v) {
+      const int r = i % kRows, tr = div_m(p, i / kRows), m = i / kRows - tr * M;  // tr: 16-row group
+      const int line = tile0 * kLines + tr * (kLines / R) + (r >> 2);
+      const int64_t row = static_cast<int64_t>(line >> 5) * 128 + (line & 31) + 32 * (r & 3);
+      if (row >= N) return;
+      float y = s * sw;
       if (GATED) {
         const float gt = s * sgate;
-        y = gt / (1.0f + expf(-gt)) * (u * sw);
-      } else {
-        y = s * sw;
+        y = gt / (1.0f + expf(-gt)) * (v * sw);
       }
       p.a.out[m * p.a.ld_out + row] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
+    };
+    // sum of output i over the warps that had a part of its tile (gated: both products),
+    // the token's scaling undone
+    auto sum = [&](int i, float& s, float& v) {
+      const int r = i % kRows, tr = div_m(p, i / kRows), m = i / kRows - tr * M, ti = tr / R;
+      s = v = 0.0f;
+      const int end = last[ti];
+      for (int w = first[ti]; w <= end; ++w) {
+        const float* q = part + (ti + w) * slot + (tr % R * M + m) * kPad + r;
+        s += q[0];
+        if (GATED) v += q[8];
+      }
+      const float up = exp2_int(down_exponent(top[m]));
+      s *= up;
+      v *= up;
+    };
+    const int outputs = nt * R * kRows * M;
+    if (p.split == 1) {
+      for (int i = threadIdx.x; i < outputs; i += kThreads) {
+        float s, v;
+        sum(i, s, v);
+        write(i, s, v);
+      }
+    } else {
+      // output i belongs to CTA (i / 32) % split of the cluster: every CTA puts its sums
+      // into the owner's memory, behind the slots, and the owner adds them in rank order
+      if (tile0 == T0) cluster_wait();  // every CTA of the cluster has started
+      float* sums = part + (p.batch + W) * slot;
+      const int shift = __ffs(p.split) - 1;                                       // split is a power of two
+      const int mine = ((outputs + 32 * p.split - 1) >> (5 + shift)) << 5;        // outputs per CTA, at most
+      for (int i = threadIdx.x; i < outputs; i += kThreads) {
+        float s, v;
+        sum(i, s, v);
+        const int b = i >> 5, owner = b & (p.split - 1), place = (b >> shift) * 32 + (i & 31);
+        const uint32_t dst = mapa_shared(smem_u32(sums + rank * mine + place), owner);
+        st_shared_cluster(dst, s);
+        if (GATED) st_shared_cluster(dst + 4 * p.split * mine, v);
+      }
+      cluster_sync();
+      for (int place = threadIdx.x; place < mine; place += kThreads) {
+        const int i = ((((place >> 5) << shift) + rank) << 5) + (place & 31);
+        if (i >= outputs) break;
+        float s = 0.0f, v = 0.0f;
+        for (int r = 0; r < p.split; ++r) {
+          s += sums[r * mine + place];
+          if (GATED) v += sums[(p.split + r) * mine + place];
+        }
+        write(i, s, v);
+      }
+      if (tile0 + p.batch < T1) cluster_sync();  // the sums may be overwritten
     }
-    __syncthreads();  // the partial sums may be overwritten
+    __syncthreads();  // the slots may be overwritten
   }
 }
 
-template <bool MX, int NT, bool GATED>
+template <bool MX, int NT, bool GATED, int WORDS, int R>
 cudaError_t launch_one(const Params& p, int grid, int threads, size_t smem, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static bool raised[64];  // per device: the kernel may use more than 48 KB (idempotent)
   if (dev >= 64 || !raised[dev]) {
-    e = cudaFuncSetAttribute(matvec_kernel<MX, NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(matvec_kernel<MX, NT, GATED, WORDS, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) raised[dev] = true;
   }
@@ -440,23 +690,54 @@ cudaError_t launch_one(const Params& p, int grid, int threads, size_t smem, cuda
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, matvec_kernel<MX, NT, GATED>, p);
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, matvec_kernel<MX, NT, GATED, WORDS, R>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// The kernel's shapes.  kNarrow: K no multiple of 64.  kPaired: more than 8 tokens, whose x
+// costs shared memory twice the reads: two 16-row groups share them.
+enum Shape { kWide, kNarrow, kPaired };
+
 template <bool MX>
-cudaError_t launch_format(const Params& p, int grid, int threads, size_t smem, cudaStream_t stream) {
-  const bool gated = p.a.gate.codes != nullptr;
-  if (p.a.M <= 8)
-    return gated ? launch_one<MX, 1, true>(p, grid, threads, smem, stream)
-                 : launch_one<MX, 1, false>(p, grid, threads, smem, stream);
-  return gated ? launch_one<MX, 2, true>(p, grid, threads, smem, stream)
-               : launch_one<MX, 2, false>(p, grid, threads, smem, stream);
+size_t ring_bytes(Shape s) {
+  return static_cast<size_t>(kWarps) * kDepth *
+         (s == kWide ? ItemBytes<MX, 8, 1>::kBytes : s == kNarrow ? ItemBytes<MX, 4, 1>::kBytes
+                                                                  : ItemBytes<MX, 4, 2>::kBytes);
+}
+
+template <bool MX, bool GATED>
+cudaError_t launch_format(const Params& p, Shape s, int grid, size_t smem, cudaStream_t stream) {
+  if (s == kWide) return launch_one<MX, 1, GATED, 8, 1>(p, grid, kThreads, smem, stream);
+  if (s == kNarrow) return launch_one<MX, 1, GATED, 4, 1>(p, grid, kThreads, smem, stream);
+  return launch_one<MX, 2, GATED, 4, 2>(p, grid, kThreads, smem, stream);
+}
+
+// Shared memory of a launch: rings, x, then slots (and a cluster's sums) for as many tiles
+// as fit, at most `tiles` of them.  0 tiles: it does not fit.
+struct Plan {
+  int tiles;
+  size_t smem;
+};
+
+Plan plan(int M, int x_units, int tiles, int split, size_t ring, int R) {
+  // a cluster's sums: 16 R per tile and token, in whole rounds of 32 and its CTAs
+  const size_t fixed = ring + static_cast<size_t>(x_units) * M * 512 + kMatvecMaxTokens * 4 +
+                       static_cast<size_t>(kWarps) * M * kPad * R * 4 + 16 +
+                       (split > 1 ? static_cast<size_t>(split) * 32 * 8 : 0);
+  const size_t tile = static_cast<size_t>(M) * kPad * R * 4 + 2 + (split > 1 ? M * 64 * R : 0);
+  if (fixed + tile > kSmem) return {0, 0};
+  const size_t room = (kSmem - fixed) / tile;
+  const int n = static_cast<size_t>(tiles) < room ? tiles : static_cast<int>(room);
+  return {n, fixed + n * tile};
 }
 
 }  // namespace
@@ -464,35 +745,59 @@ cudaError_t launch_format(const Params& p, int grid, int threads, size_t smem, c
 cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
-  p.chunks = static_cast<int>((a.K + kChunk - 1) / kChunk);
-  const int W = p.chunks < kMaxWarps ? p.chunks : kMaxWarps;
-  const int per_sm = kMaxWarps / W;  // CTAs of short rows share an SM
+  const bool gated = a.gate.codes != nullptr;
+  const Shape shape = a.M > 8 ? kPaired : a.K % 64 == 0 ? kWide : kNarrow;
+  const int R = shape == kPaired ? 2 : 1;
   const int64_t tail = a.N % 128;
-  p.lines = a.N / 128 * 32 + (tail < 32 ? tail : 32);
-  p.atoms = ((a.K / (a.mx ? 32 : 16)) + 3) / 4;
-  const int last_blocks = static_cast<int>(a.K / 32 - (p.chunks - 1) * int64_t{4});
-  p.last_mask = last_blocks == 4 ? 0xFFFFFFFFu : (1u << (8 * last_blocks)) - 1u;
-  int dev = 0, sms = 148;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int64_t slots = static_cast<int64_t>(sms) * per_sm;
-  const int grid = static_cast<int>(p.lines < slots ? p.lines : slots);
-  // x: as many of a warp's chunks as its share of shared memory holds, in equal slices
-  const int per_warp = (p.chunks + W - 1) / W;
-  int most = kXBytes / (a.M * 256);
-  if (most > kMaxSlice) most = kMaxSlice;
-  const int slices = (per_warp + most - 1) / most;
-  p.slice = (per_warp + slices - 1) / slices;
-  // partial sums: as many tiles as the rest holds
-  const size_t x_bytes = static_cast<size_t>(W) * p.slice * a.M * 256;
-  const size_t tile_bytes = static_cast<size_t>(W) * a.M * kPad * sizeof(float);
-  const int lines_per_tile = a.gate.codes ? 2 : 4;
-  const int64_t tiles = ((p.lines + grid - 1) / grid + lines_per_tile - 1) / lines_per_tile;
-  const int64_t room = static_cast<int64_t>((kSmem / per_sm - x_bytes) / tile_bytes);
-  p.batch = static_cast<int>(tiles < room ? tiles : room);
-  const size_t smem = x_bytes + p.batch * tile_bytes;
-  return a.mx ? launch_format<true>(p, grid, W * 32, smem, stream) : launch_format<false>(p, grid, W * 32, smem, stream);
+  const int lines_per_tile = (gated ? 2 : 4) * R;
+  const int64_t lines = a.N / 128 * 32 + (tail < 32 ? tail : 32);  // neighbour lines, 4 rows each
+  p.tiles = static_cast<int>((lines + lines_per_tile - 1) / lines_per_tile);
+  p.units = static_cast<int>((a.K + kUnit - 1) / kUnit);
+  p.atoms = static_cast<int>((a.K / (a.mx ? 32 : 16) + 3) / 4);
+  const size_t ring = a.mx ? ring_bytes<true>(shape) : ring_bytes<false>(shape);
+  // CTAs per cluster: the fewest items for the busiest CTA among the splits whose part of x
+  // fits.  Clusters that the GPU holds at a time, of CTAs that fill an SM: 148, 74, 33, 15.
+  static const int kSplits[4] = {1, 2, 4, 8}, kGroups[4] = {148, 74, 33, 15};
+  int64_t best = -1;
+  int groups = 1;
+  size_t smem = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int s = kSplits[i], n = p.tiles < kGroups[i] ? p.tiles : kGroups[i];
+    const int x_units = (p.units + s - 1) / s, tiles = (p.tiles + n - 1) / n;
+    const Plan q = plan(a.M, x_units, tiles, s, ring, R);
+    // (in quarters of the time of an item of 16 x 256 weights: a unit of a token to stage 1, a
+    // cluster's barriers, and its wait for the slowest CTA, 8)
+    const int64_t items = static_cast<int64_t>(tiles) * x_units * R, pieces = static_cast<int64_t>(x_units) * a.M;
+    const int64_t cost = (items * 4 + kWarps - 1) / kWarps + (pieces + kWarps - 1) / kWarps + (s > 1 ? 8 : 0);
+    if (q.tiles == 0 || s > p.units || (best >= 0 && cost >= best)) continue;
+    best = cost;
+    p.split = s;
+    p.batch = q.tiles;
+    p.x_units = x_units;
+    groups = n;
+    smem = q.smem;
+  }
+  if (best < 0) {  // x of this many tokens fits no split: half of them at a time
+    if (a.M == 1) return cudaErrorInvalidValue;
+    MatvecArgs first = a, second = a;
+    first.M = a.M / 2;
+    second.M = a.M - first.M;
+    const int64_t bytes = a.x_scales ? 1 : 2;
+    second.x = static_cast<const uint8_t*>(a.x) + first.M * a.ld_x * bytes;
+    // (an MXFP8 scale row: 16 bytes further in the 128 x 4 tiles, K / 32 bytes in rows)
+    if (a.x_scales) second.x_scales = a.x_scales + first.M * (a.x_swizzled ? 16 : a.K / 32);
+    second.out = a.out + first.M * a.ld_out;
+    const cudaError_t e = launch_matvec(first, stream);
+    return e != cudaSuccess ? e : launch_matvec(second, stream);
+  }
+  p.m_inv = static_cast<uint32_t>(((uint64_t{1} << 32) + a.M - 1) / a.M);
+  p.tiles_q = p.tiles / groups, p.tiles_r = p.tiles % groups;
+  p.units_q = p.units / p.split, p.units_r = p.units % p.split;
+  const int grid = groups * p.split;
+  if (a.mx) return gated ? launch_format<true, true>(p, shape, grid, smem, stream)
+                         : launch_format<true, false>(p, shape, grid, smem, stream);
+  return gated ? launch_format<false, true>(p, shape, grid, smem, stream)
+               : launch_format<false, false>(p, shape, grid, smem, stream);
 }
 
 }  // namespace nvfp4
