@@ -31,6 +31,8 @@
 // workspace, the same bits on every call.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "layer_ops.h"
 #include "ptx.cuh"
 
@@ -40,7 +42,7 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kDepth = 2;        // weight items in flight per warp (3 and 4: no faster, less room for x)
-constexpr int kPad = 20;         // floats per token of a 16-row partial (padded: conflict-free)
+constexpr int kPad = 16;         // floats per token of a 16-row partial
 constexpr int kUnit = 256;       // K is divided in units of this between a cluster's CTAs
 constexpr int kSmem = 226 * 1024;
 
@@ -52,6 +54,8 @@ struct Params {
   int batch;          // tiles between two reductions
   int split;          // CTAs of a cluster that share tiles, each a part of K
   int x_units;        // units of a part, at most
+  int sums_at;        // a cluster's sums, bytes into shared memory
+  bool sums_over_x;   // they take the place of x (one batch)
   uint32_t m_inv;     // ceil(2^32 / M): x / M = mulhi(x, m_inv) for the small x it is used on
   int tiles_q, tiles_r, units_q, units_r;  // tiles per CTA (cluster) and units per part, and remainders
 };
@@ -151,8 +155,12 @@ __device__ __forceinline__ void fp8_values(uint32_t lo4, uint32_t hi4, float s, 
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_shared_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_shared_cluster(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   uint4 v;
@@ -463,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     }
     copies_commit();  // (empty past the end: the wait counts groups)
   };
-  if (p.split > 1) cluster_arrive();  // waited for before the first store into another CTA
-  __syncthreads();                    // `top` is zeroed
+  if (p.split > 1 && !p.sums_over_x) cluster_arrive();  // waited for before the first store into another CTA
+  __syncthreads();  // `top` is zeroed
   segment();
   grid_dependency_wait();
   grid_dependents_launch();
@@ -487,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     x_at[n] = smem_u32(xs + m * 32 + t);
     x_flip[n] = (m & 1) * 64;
   }
+  const float sw = p.a.w.gs ? *p.a.w.gs : 1.0f, sgate = GATED && p.a.gate.gs ? *p.a.gate.gs : 1.0f;
   int at = 0;  // the slot's offset in the ring
   for (int tile0 = T0; tile0 < T1; tile0 += p.batch) {
     const int nt = min(p.batch, T1 - tile0);
@@ -606,65 +615,80 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       ++ti;
     }
     __syncthreads();
-    constexpr int kRows = GATED ? 8 : 16;  // outputs of a 16-row group per token
-    const float sw = p.a.w.gs ? *p.a.w.gs : 1.0f, sgate = GATED && p.a.gate.gs ? *p.a.gate.gs : 1.0f;
-    auto write = [&](int i, float s, float v) {
-      const int r = i % kRows, tr = div_m(p, i / kRows), m = i / kRows - tr * M;  // tr: 16-row group
-      const int line = tile0 * kLines + tr * (kLines / R) + (r >> 2);
-      const int64_t row = static_cast<int64_t>(line >> 5) * 128 + (line & 31) + 32 * (r & 3);
-      if (row >= N) return;
-      float y = s * sw;
-      if (GATED) {
-        const float gt = s * sgate;
-        y = gt / (1.0f + expf(-gt)) * (v * sw);
-      }
-      p.a.out[m * p.a.ld_out + row] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
-    };
-    // sum of output i over the warps that had a part of its tile (gated: both products),
-    // the token's scaling undone
-    auto sum = [&](int i, float& s, float& v) {
-      const int r = i % kRows, tr = div_m(p, i / kRows), m = i / kRows - tr * M, ti = tr / R;
-      s = v = 0.0f;
-      const int end = last[ti];
-      for (int w = first[ti]; w <= end; ++w) {
-        const float* q = part + (ti + w) * slot + (tr % R * M + m) * kPad + r;
-        s += q[0];
-        if (GATED) v += q[8];
+    // Outputs, four to a thread: i = (group of 16 rows, token, line), the line's rows of the
+    // four quarters.
+    constexpr int kOut = GATED ? 2 : 4;  // lines of a 16-row group
+    const int outputs = nt * R * kOut * M;
+    const int out_line = lane % kOut;
+    // sums of output i over the warps that had a part of its tile (gated: both products), the
+    // token's scaling undone
+    auto sum = [&](int i, float4& s, float4& v) {
+      const int tr = div_m(p, i / kOut), m = i / kOut - tr * M, ti = tr / R;
+      const int w0 = first[ti], w1 = last[ti];
+      const float* q = part + ((ti + w0) * R + tr % R) * (M * kPad) + m * kPad + 4 * out_line;
+      s = *reinterpret_cast<const float4*>(q);
+      if (GATED) v = *reinterpret_cast<const float4*>(q + 8);
+      for (int w = w0; w < w1; ++w) {
+        q += slot;
+        s = add4(s, *reinterpret_cast<const float4*>(q));
+        if (GATED) v = add4(v, *reinterpret_cast<const float4*>(q + 8));
       }
       const float up = exp2_int(down_exponent(top[m]));
-      s *= up;
-      v *= up;
+      s = make_float4(s.x * up, s.y * up, s.z * up, s.w * up);
+      if (GATED) v = make_float4(v.x * up, v.y * up, v.z * up, v.w * up);
     };
-    const int outputs = nt * R * kRows * M;
+    auto write = [&](int i, float4 s, float4 v) {
+      const int tr = div_m(p, i / kOut), m = i / kOut - tr * M;
+      const int line = tile0 * kLines + tr * (kLines / R) + out_line;
+      const int row = (line >> 5) * 128 + (line & 31);
+      uint16_t* const y = p.a.out + m * p.a.ld_out + row;
+      const float ss[4] = {s.x, s.y, s.z, s.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f = ss[k] * sw;
+        if (GATED) {
+          const float gt = ss[k] * sgate;
+          f = gt / (1.0f + expf(-gt)) * (vv[k] * sw);
+        }
+        if (row + 32 * k < N) y[32 * k] = static_cast<uint16_t>(pack_bf16(f, 0.0f));
+      }
+    };
     if (p.split == 1) {
       for (int i = threadIdx.x; i < outputs; i += kThreads) {
-        float s, v;
+        float4 s, v = {};
         sum(i, s, v);
         write(i, s, v);
       }
     } else {
-      // output i belongs to CTA (i / 32) % split of the cluster: every CTA puts its sums
-      // into the owner's memory, behind the slots, and the owner adds them in rank order
-      if (tile0 == T0) cluster_wait();  // every CTA of the cluster has started
-      float* sums = part + (p.batch + W) * slot;
-      const int shift = __ffs(p.split) - 1;                                       // split is a power of two
-      const int mine = ((outputs + 32 * p.split - 1) >> (5 + shift)) << 5;        // outputs per CTA, at most
-      for (int i = threadIdx.x; i < outputs; i += kThreads) {
-        float s, v;
-        sum(i, s, v);
-        const int b = i >> 5, owner = b & (p.split - 1), place = (b >> shift) * 32 + (i & 31);
-        const uint32_t dst = mapa_shared(smem_u32(sums + rank * mine + place), owner);
-        st_shared_cluster(dst, s);
-        if (GATED) st_shared_cluster(dst + 4 * p.split * mine, v);
+      // 32 threads' outputs at a time belong to one CTA of the cluster in turn: every CTA puts
+      // its sums into the owner's memory (that of x when it is no longer needed), 16 bytes a
+      // store, and the owner adds them in rank order
+      if (p.sums_over_x) {
+        cluster_sync();  // every CTA is through with its items
+      } else if (tile0 == T0) {
+        cluster_wait();  // every CTA has started
+      }
+      float4* sums = reinterpret_cast<float4*>(smem + p.sums_at);
+      const int shift = __ffs(p.split) - 1;                                 // split is a power of two
+      const int mine = ((outputs + 32 * p.split - 1) >> (5 + shift)) << 5;  // outputs per CTA, at most
+      const uint32_t my_sums = smem_u32(sums + rank * mine + lane);
+      for (int b = warp; b * 32 < outputs; b += W) {
+        if (b * 32 + lane < outputs) {
+          float4 s, v;
+          sum(b * 32 + lane, s, v);
+          const uint32_t dst = mapa_shared(my_sums + (b >> shift) * 512, b & (p.split - 1));
+          st_shared_cluster(dst, s);
+          if (GATED) st_shared_cluster(dst + 16 * p.split * mine, v);
+        }
       }
       cluster_sync();
-      for (int place = threadIdx.x; place < mine; place += kThreads) {
-        const int i = ((((place >> 5) << shift) + rank) << 5) + (place & 31);
+      for (int b = warp; b * 32 < mine; b += W) {
+        const int i = ((b << shift) + rank) * 32 + lane;
         if (i >= outputs) break;
-        float s = 0.0f, v = 0.0f;
-        for (int r = 0; r < p.split; ++r) {
-          s += sums[r * mine + place];
-          if (GATED) v += sums[(p.split + r) * mine + place];
+        float4 s = {}, v = {};
+        for (int k = 0; k < p.split; ++k) {
+          s = add4(s, sums[k * mine + b * 32 + lane]);
+          if (GATED) v = add4(v, sums[(p.split + k) * mine + b * 32 + lane]);
         }
         write(i, s, v);
       }
@@ -721,23 +745,29 @@ cudaError_t launch_format(const Params& p, Shape s, int grid, size_t smem, cudaS
   return launch_one<MX, 2, GATED, 4, 2>(p, grid, kThreads, smem, stream);
 }
 
-// Shared memory of a launch: rings, x, then slots (and a cluster's sums) for as many tiles
-// as fit, at most `tiles` of them.  0 tiles: it does not fit.
+// Shared memory of a launch: rings, x, then slots for as many tiles as fit, at most `tiles`
+// of them (0: not even one), and a cluster's sums -- in x's place when that, and only that,
+// lets one batch be all.
 struct Plan {
   int tiles;
-  size_t smem;
+  size_t smem, sums_at;
+  bool over_x;
 };
 
 Plan plan(int M, int x_units, int tiles, int split, size_t ring, int R) {
-  // a cluster's sums: 16 R per tile and token, in whole rounds of 32 and its CTAs
-  const size_t fixed = ring + static_cast<size_t>(x_units) * M * 512 + kMatvecMaxTokens * 4 +
-                       static_cast<size_t>(kWarps) * M * kPad * R * 4 + 16 +
-                       (split > 1 ? static_cast<size_t>(split) * 32 * 8 : 0);
-  const size_t tile = static_cast<size_t>(M) * kPad * R * 4 + 2 + (split > 1 ? M * 64 * R : 0);
-  if (fixed + tile > kSmem) return {0, 0};
-  const size_t room = (kSmem - fixed) / tile;
-  const int n = static_cast<size_t>(tiles) < room ? tiles : static_cast<int>(room);
-  return {n, fixed + n * tile};
+  const size_t x = static_cast<size_t>(x_units) * M * 512, slot = static_cast<size_t>(M) * kPad * R * 4;
+  const size_t fixed = ring + x + kMatvecMaxTokens * 4 + 16 + kWarps * slot;
+  if (fixed + slot + 2 > kSmem) return {0, 0, 0, false};
+  const int slots = static_cast<int>(std::min<size_t>(tiles, (kSmem - fixed) / (slot + 2)));
+  if (split == 1) return {slots, fixed + slots * (slot + 2), 0, false};
+  // sums: 16 R per tile and token, in whole rounds of 32 threads' and the cluster's CTAs
+  const size_t round = static_cast<size_t>(split) * 32 * 16 * 2 + 16, sum = static_cast<size_t>(M) * 64 * R;
+  size_t n = fixed + round > kSmem ? 0 : (kSmem - fixed - round) / (slot + 2 + sum);
+  if (n < static_cast<size_t>(tiles) && slots == tiles && tiles * sum + round <= x)
+    return {tiles, fixed + tiles * (slot + 2), ring, true};
+  n = std::min<size_t>(n, tiles);
+  const size_t at = (fixed + n * (slot + 2) + 15) / 16 * 16;
+  return {static_cast<int>(n), at + round + n * sum, at, false};
 }
 
 }  // namespace
@@ -776,6 +806,8 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
     p.x_units = x_units;
     groups = n;
     smem = q.smem;
+    p.sums_at = static_cast<int>(q.sums_at);
+    p.sums_over_x = q.over_x;
   }
   if (best < 0) {  // x of this many tokens fits no split: half of them at a time
     if (a.M == 1) return cudaErrorInvalidValue;
