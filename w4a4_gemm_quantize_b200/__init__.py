@@ -111,12 +111,12 @@ def _check(status: int, where: str):
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 @dataclass
@@ -373,16 +373,14 @@ class MXFP8Tensor:
 
 
 class _On:
-    """The device and stream of one call on `tensor`: makes the tensor's device current, and where the caller
-    names a stream, allocates on it (a temporary is not reused before that stream is through with it)."""
+    """The device and stream of one call: makes the tensors' device current, and where the caller names a stream,
+    allocates on it (a temporary is not reused before that stream is through with it)."""
 
-    def __init__(self, tensor: torch.Tensor, stream):
-        self.contexts = []
-        if tensor.device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(tensor.device))
+    def __init__(self, device: torch.device, stream):
+        self.contexts = [torch.cuda.device(device)]
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=tensor.device)
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
             self.contexts.append(torch.cuda.stream(stream))
 
     def __enter__(self):
@@ -394,77 +392,83 @@ class _On:
             c.__exit__(*exc)
 
 
-def _matrix(t: torch.Tensor, name: str, device=None, shape=None) -> int:
-    """Checks a BF16 matrix argument and returns its row stride (a single row's is its length, rounded up)."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+def _elsewhere(x, stream) -> bool:
+    """Whether a call on x has to leave the current device or stream."""
+    return stream is not None or x.get_device() != torch._C._cuda_getDevice()
+
+
+def _ld(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None) -> int:
+    """Checks a BF16 matrix argument (of `shape`, on `like`'s device) and returns its row stride (a single row's is
+    its length, rounded up)."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D bfloat16 CUDA tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if like is not None and t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    ld, step = t.stride()
+    if step != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must be row-major (stride 1 along its rows)")
-    return -(-cols // 16) * 16 if rows <= 1 else t.stride(0)
+    return ld if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
 
 
-def _like(t: Optional[torch.Tensor], name: str, dtype, numel: int, device) -> None:
-    if t is not None and (t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {device}")
+def _like(t: torch.Tensor, name: str, dtype, numel: int, like: torch.Tensor) -> None:
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {like.device}")
 
 
-def _row_output(fmt: int, layout: int, rows: int, cols: int, device, out, global_scale):
-    """The output tensors of a row operator: (what the caller gets, data, row stride, scales, tensor scale)."""
+def _swizzled_bytes(rows: int, blocks: int) -> int:
+    """nvfp4_scales_bytes / mxfp4_scales_bytes of the SWIZZLED layout."""
+    return (rows + 127) // 128 * 128 * ((blocks + 3) // 4 * 4)
+
+
+def _row_output(fmt: int, layout: int, x: torch.Tensor, out, global_scale):
+    """The output of a row operator on x's shape: (what the caller gets, data, row stride, scales, tensor scale)."""
+    rows, cols = shape = x.shape
     if global_scale is not None:
         if fmt != OUT_NVFP4:
             raise ValueError("global_scale is NVFP4's tensor scale; this format has none")
-        _like(global_scale, "global_scale", torch.float32, 1, device)
+        _like(global_scale, "global_scale", torch.float32, 1, x)
     if fmt == OUT_BF16:
         if out is None:
-            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
-        return out, out, _matrix(out, "out", device, (rows, cols)), None, None
+            out = x.new_empty(shape)
+            return out, out, cols if rows > 1 else -(-cols // 16) * 16, None, None
+        return out, out, _ld(out, "out", shape, x), None, None
     block = 16 if fmt == OUT_NVFP4 else 32
-    if cols % block:
+    blocks = cols // block
+    if blocks * block != cols:
         raise ValueError(f"{cols} columns are no whole number of {block}-value blocks")
-    lib = load_library()
-    nsf = (lib.nvfp4_scales_bytes if block == 16 else lib.mxfp4_scales_bytes)(rows, cols, layout)
-    kind = {OUT_MXFP8: MXFP8Tensor, OUT_MXFP4: MXFP4Tensor, OUT_NVFP4: NVFP4Tensor}[fmt]
-    width, dtype = (cols, torch.float8_e4m3fn) if fmt == OUT_MXFP8 else (cols // 2, torch.uint8)
-    if out is None:
-        codes = torch.empty((rows, width), dtype=dtype, device=device)
-        scales = torch.empty((rows, cols // block) if layout == SF_LINEAR else (nsf,), dtype=torch.uint8, device=device)
-        if fmt == OUT_NVFP4:
-            gs = torch.empty(1, dtype=torch.float32, device=device)
-            out = NVFP4Tensor(codes, scales, gs, rows, cols, layout)
-        else:
-            out = kind(codes, scales, rows, cols, layout)
+    if fmt == OUT_MXFP8:
+        kind, width, dtype = MXFP8Tensor, cols, torch.float8_e4m3fn
     else:
-        if not isinstance(out, kind) or (out.rows, out.cols, out.layout) != (rows, cols, layout):
-            raise ValueError(f"out must be a {kind.__name__} of {rows} x {cols} with the asked scale layout")
-        _like(out.codes, "out.codes", dtype, rows * width, device)
-        _like(out.scales, "out.scales", torch.uint8, nsf, device)
-        if fmt == OUT_NVFP4:
-            _like(out.global_scale, "out.global_scale", torch.float32, 1, device)
-    return out, out.codes, cols, out.scales, out.global_scale if fmt == OUT_NVFP4 else None
+        kind, width, dtype = NVFP4Tensor if block == 16 else MXFP4Tensor, cols // 2, torch.uint8
+    if out is None:
+        codes = x.new_empty((rows, width), dtype=dtype)
+        scales = x.new_empty((rows, blocks) if layout == SF_LINEAR else _swizzled_bytes(rows, blocks), dtype=torch.uint8)
+        if fmt != OUT_NVFP4:
+            return kind(codes, scales, rows, cols, layout), codes, cols, scales, None
+        gs = x.new_empty(1, dtype=torch.float32)
+        return NVFP4Tensor(codes, scales, gs, rows, cols, layout), codes, cols, scales, gs
+    if not isinstance(out, kind) or (out.rows, out.cols, out.layout) != (rows, cols, layout):
+        raise ValueError(f"out must be a {kind.__name__} of {rows} x {cols} with the asked scale layout")
+    _like(out.codes, "out.codes", dtype, rows * width, x)
+    _like(out.scales, "out.scales", torch.uint8,
+          rows * blocks if layout == SF_LINEAR else _swizzled_bytes(rows, blocks), x)
+    if fmt != OUT_NVFP4:
+        return out, out.codes, cols, out.scales, None
+    _like(out.global_scale, "out.global_scale", torch.float32, 1, x)
+    return out, out.codes, cols, out.scales, out.global_scale
 
 
-def _row_workspace(fmt: int, global_scale, workspace, device):
+def _row_workspace(fmt: int, global_scale, workspace, x):
     """(workspace, its bytes): only NVFP4 with a computed tensor scale needs one."""
-    if workspace is None and fmt == OUT_NVFP4 and global_scale is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=device)
     if workspace is None:
-        return None, 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
+        if fmt != OUT_NVFP4 or global_scale is not None:
+            return None, 0
+        return x.new_empty(256, dtype=torch.uint8), 256
+    if workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {x.device}")
     return workspace, workspace.numel() * workspace.element_size()
-
-
-def _at(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _choice(table, value, name):
@@ -487,26 +491,32 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     tensor scale is `global_scale` (a device float) or computed from v.  Returns the output, or with a residual
     (output, h); residual_out may be `residual` itself to update the stream in place."""
     fmt, lay = _choice(_FORMATS, out_format, "out_format"), _choice(_LAYOUTS, layout, "layout")
-    ld_x = _matrix(x, "x")
-    rows, cols = x.shape
-    dev = x.device
-    if (residual is None) and residual_out is not None:
-        raise ValueError("residual_out without a residual")
+    ld_x = _ld(x, "x")
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return rms_norm(x, weight, residual, eps, weight_offset, out_format, layout, global_scale, out,
+                            residual_out, workspace)
+    shape = rows, cols = x.shape
+    result, data, ld_out, scales, gs = _row_output(fmt, lay, x, out, global_scale)
     if weight is not None:
-        _like(weight, "weight", torch.bfloat16, cols, dev)
-    with _On(x, stream):
-        result, data, ld_out, scales, gs = _row_output(fmt, lay, rows, cols, dev, out, global_scale)
-        ld_r = ld_ro = 0
-        if residual is not None:
-            ld_r = _matrix(residual, "residual", dev, x.shape)
-            if residual_out is None:
-                residual_out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-            ld_ro = _matrix(residual_out, "residual_out", dev, x.shape)
-        workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, dev)
-        _check(load_library().nvfp4_rms_norm(_at(x), rows, cols, ld_x, _at(residual), ld_r, _at(residual_out), ld_ro,
-                                             _at(weight), weight_offset, eps, fmt, lay, _at(global_scale), _at(data),
-                                             ld_out, _at(scales), _at(gs), _at(workspace), ws_bytes,
-                                             _raw_stream(dev)), "nvfp4_rms_norm")
+        _like(weight, "weight", torch.bfloat16, cols, x)
+    ld_r = ld_ro = 0
+    if residual is not None:
+        ld_r = _ld(residual, "residual", shape, x)
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+            ld_ro = cols if rows > 1 else ld_r
+        else:
+            ld_ro = _ld(residual_out, "residual_out", shape, x)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, x)
+    st = load_library().nvfp4_rms_norm(x.data_ptr(), rows, cols, ld_x, _ptr(residual), ld_r, _ptr(residual_out), ld_ro,
+                                       _ptr(weight), weight_offset, eps, fmt, lay, _ptr(global_scale),
+                                       data.data_ptr(), ld_out, _ptr(scales), _ptr(gs), _ptr(workspace), ws_bytes,
+                                       _stream(None))
+    if st:
+        _check(st, "nvfp4_rms_norm")
     return result if residual is None else (result, residual_out)
 
 
@@ -516,16 +526,19 @@ def silu_mul(gate: torch.Tensor, up: torch.Tensor, out_format: str = "bf16", lay
     """silu(gate) * up of two 2-D BF16 tensors (strided views, such as the halves of one product, are fine), written
     as `out_format` like rms_norm's output (see nvfp4_silu_mul in include/nvfp4.h)."""
     fmt, lay = _choice(_FORMATS, out_format, "out_format"), _choice(_LAYOUTS, layout, "layout")
-    ld_g = _matrix(gate, "gate")
+    ld_g = _ld(gate, "gate")
+    if _elsewhere(gate, stream):
+        with _On(gate.device, stream):
+            return silu_mul(gate, up, out_format, layout, global_scale, out, workspace)
     rows, cols = gate.shape
-    dev = gate.device
-    ld_u = _matrix(up, "up", dev, gate.shape)
-    with _On(gate, stream):
-        result, data, ld_out, scales, gs = _row_output(fmt, lay, rows, cols, dev, out, global_scale)
-        workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, dev)
-        _check(load_library().nvfp4_silu_mul(_at(gate), ld_g, _at(up), ld_u, rows, cols, fmt, lay, _at(global_scale),
-                                             _at(data), ld_out, _at(scales), _at(gs), _at(workspace), ws_bytes,
-                                             _raw_stream(dev)), "nvfp4_silu_mul")
+    ld_u = _ld(up, "up", gate.shape, gate)
+    result, data, ld_out, scales, gs = _row_output(fmt, lay, gate, out, global_scale)
+    workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, gate)
+    st = load_library().nvfp4_silu_mul(gate.data_ptr(), ld_g, up.data_ptr(), ld_u, rows, cols, fmt, lay,
+                                       _ptr(global_scale), data.data_ptr(), ld_out, _ptr(scales), _ptr(gs),
+                                       _ptr(workspace), ws_bytes, _stream(None))
+    if st:
+        _check(st, "nvfp4_silu_mul")
     return result
 
 
@@ -534,38 +547,42 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
     (NVFP4Tensor or MXFP4Tensor, N x K, swizzled scales); the activation is not rounded to 4 bits.  With w_gate, a
     second weight of the same kind and shape: silu(x w_gate^T) * (x w^T) in one pass.  More rows: use linear,
     nvfp4_gemm or mxfp4_gemm."""
-    fp8 = isinstance(x, MXFP8Tensor)
-    dev = x.codes.device if fp8 else x.device
-    if fp8:
-        if not x.codes.is_cuda:
-            raise ValueError("x must be on a CUDA device")
-        M, K, ld_x, x_lay = x.rows, x.cols, x.cols, _choice(_LAYOUTS, x.layout, "x.layout")
-        _like(x.codes, "x.codes", torch.float8_e4m3fn, M * K, dev)
-        _like(x.scales, "x.scales", torch.uint8, mxfp8_scales_bytes(M, K, x_lay), dev)
-        xd, xs = x.codes, x.scales
+    if isinstance(x, torch.Tensor):
+        data, scales, x_lay, ld_x = x, None, SF_SWIZZLED, _ld(x, "x")
+        M, K = x.shape
     else:
-        ld_x = _matrix(x, "x")
-        (M, K), xd, xs, x_lay = x.shape, x, None, SF_SWIZZLED
+        if not isinstance(x, MXFP8Tensor) or not x.codes.is_cuda:
+            raise ValueError("x must be a 2-D bfloat16 CUDA tensor or an MXFP8Tensor on a CUDA device")
+        data, scales, M, K = x.codes, x.scales, x.rows, x.cols
+        ld_x, x_lay = K, _choice(_LAYOUTS, x.layout, "x.layout")
+        _like(data, "x.codes", torch.float8_e4m3fn, M * K, data)
+        _like(scales, "x.scales", torch.uint8,
+              M * (K // 32) if x_lay == SF_LINEAR else _swizzled_bytes(M, K // 32), data)
     nvfp4 = isinstance(w, NVFP4Tensor)
     if not nvfp4 and not isinstance(w, MXFP4Tensor):
         raise ValueError("w must be an NVFP4Tensor or an MXFP4Tensor")
-    N = w.rows
+    N, dev = w.rows, data.get_device()
     for t in (w,) if w_gate is None else (w, w_gate):
-        if type(t) is not type(w) or (t.rows, t.cols) != (N, K) or t.layout != SF_SWIZZLED or t.codes.device != dev:
+        if type(t) is not type(w) or t.rows != N or t.cols != K or t.layout != SF_SWIZZLED or t.codes.get_device() != dev:
             raise ValueError("the weights must share K with x, one kind and shape, x's device, and have swizzled scales")
-    with _On(xd, stream):
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        ld_out = max(_matrix(out, "out", dev, (M, N)), N)
-        lib, s = load_library(), _raw_stream(dev)
-        gc, gsc = (None, None) if w_gate is None else (w_gate.codes.data_ptr(), w_gate.scales.data_ptr())
-        if nvfp4:
-            gg = None if w_gate is None else w_gate.global_scale.data_ptr()
-            st = lib.nvfp4_matvec(xd.data_ptr(), _at(xs), x_lay, M, K, ld_x, w.codes.data_ptr(), w.scales.data_ptr(),
-                                  w.global_scale.data_ptr(), gc, gsc, gg, N, out.data_ptr(), ld_out, s)
-        else:
-            st = lib.mxfp4_matvec(xd.data_ptr(), _at(xs), x_lay, M, K, ld_x, w.codes.data_ptr(), w.scales.data_ptr(),
-                                  gc, gsc, N, out.data_ptr(), ld_out, s)
+    if _elsewhere(data, stream):
+        with _On(data.device, stream):
+            return matvec(x, w, w_gate, out)
+    if out is None:
+        out = data.new_empty((M, N), dtype=torch.bfloat16)
+        ld_out = N
+    else:
+        ld_out = max(_ld(out, "out", (M, N), data), N)
+    gc, gsc = (None, None) if w_gate is None else (w_gate.codes.data_ptr(), w_gate.scales.data_ptr())
+    if nvfp4:
+        st = load_library().nvfp4_matvec(data.data_ptr(), _ptr(scales), x_lay, M, K, ld_x, w.codes.data_ptr(),
+                                         w.scales.data_ptr(), w.global_scale.data_ptr(), gc, gsc,
+                                         None if w_gate is None else w_gate.global_scale.data_ptr(), N,
+                                         out.data_ptr(), ld_out, _stream(None))
+    else:
+        st = load_library().mxfp4_matvec(data.data_ptr(), _ptr(scales), x_lay, M, K, ld_x, w.codes.data_ptr(),
+                                         w.scales.data_ptr(), gc, gsc, N, out.data_ptr(), ld_out, _stream(None))
+    if st:
         _check(st, "nvfp4_matvec" if nvfp4 else "mxfp4_matvec")
     return out
 
