@@ -400,16 +400,19 @@ def _elsewhere(x, stream) -> bool:
 def _ld(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None) -> int:
     """Checks a BF16 matrix argument (of `shape`, on `like`'s device) and returns its row stride (a single row's is
     its length, rounded up)."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+    own = t.shape
+    if t.dtype is not torch.bfloat16 or len(own) != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D bfloat16 CUDA tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if like is not None and t.get_device() != like.get_device():
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if shape is not None:
+        if own != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(own)}")
+        if t.get_device() != like.get_device():
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    rows, cols = own
     ld, step = t.stride()
-    if step != 1 and t.shape[1] > 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must be row-major (stride 1 along its rows)")
-    return ld if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+    return ld if rows > 1 else -(-cols // 16) * 16
 
 
 def _like(t: torch.Tensor, name: str, dtype, numel: int, like: torch.Tensor) -> None:
@@ -431,7 +434,7 @@ def _row_output(fmt: int, layout: int, x: torch.Tensor, out, global_scale):
         _like(global_scale, "global_scale", torch.float32, 1, x)
     if fmt == OUT_BF16:
         if out is None:
-            out = x.new_empty(shape)
+            out = torch.empty(rows, cols, dtype=torch.bfloat16, device=x.device)
             return out, out, cols if rows > 1 else -(-cols // 16) * 16, None, None
         return out, out, _ld(out, "out", shape, x), None, None
     block = 16 if fmt == OUT_NVFP4 else 32
@@ -443,11 +446,15 @@ def _row_output(fmt: int, layout: int, x: torch.Tensor, out, global_scale):
     else:
         kind, width, dtype = NVFP4Tensor if block == 16 else MXFP4Tensor, cols // 2, torch.uint8
     if out is None:
-        codes = x.new_empty((rows, width), dtype=dtype)
-        scales = x.new_empty((rows, blocks) if layout == SF_LINEAR else _swizzled_bytes(rows, blocks), dtype=torch.uint8)
+        dev = x.device
+        codes = torch.empty(rows, width, dtype=dtype, device=dev)
+        if layout == SF_LINEAR:
+            scales = torch.empty(rows, blocks, dtype=torch.uint8, device=dev)
+        else:
+            scales = torch.empty(_swizzled_bytes(rows, blocks), dtype=torch.uint8, device=dev)
         if fmt != OUT_NVFP4:
             return kind(codes, scales, rows, cols, layout), codes, cols, scales, None
-        gs = x.new_empty(1, dtype=torch.float32)
+        gs = torch.empty(1, dtype=torch.float32, device=dev)
         return NVFP4Tensor(codes, scales, gs, rows, cols, layout), codes, cols, scales, gs
     if not isinstance(out, kind) or (out.rows, out.cols, out.layout) != (rows, cols, layout):
         raise ValueError(f"out must be a {kind.__name__} of {rows} x {cols} with the asked scale layout")
@@ -465,17 +472,16 @@ def _row_workspace(fmt: int, global_scale, workspace, x):
     if workspace is None:
         if fmt != OUT_NVFP4 or global_scale is not None:
             return None, 0
-        return x.new_empty(256, dtype=torch.uint8), 256
+        return torch.empty(256, dtype=torch.uint8, device=x.device), 256
     if workspace.device != x.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {x.device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
 def _choice(table, value, name):
-    try:
+    if isinstance(value, (str, int)) and value in table:
         return table[value]
-    except (KeyError, TypeError):
-        raise ValueError(f"{name} must be one of {[k for k in table if isinstance(k, str)]}, got {value!r}") from None
+    raise ValueError(f"{name} must be one of {[k for k in table if isinstance(k, str)]}, got {value!r}")
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -504,7 +510,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     if residual is not None:
         ld_r = _ld(residual, "residual", shape, x)
         if residual_out is None:
-            residual_out = torch.empty_like(x)
+            residual_out = torch.empty(rows, cols, dtype=torch.bfloat16, device=x.device)
             ld_ro = cols if rows > 1 else ld_r
         else:
             ld_ro = _ld(residual_out, "residual_out", shape, x)
@@ -569,7 +575,7 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
         with _On(data.device, stream):
             return matvec(x, w, w_gate, out)
     if out is None:
-        out = data.new_empty((M, N), dtype=torch.bfloat16)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=data.device)
         ld_out = N
     else:
         ld_out = max(_ld(out, "out", (M, N), data), N)

@@ -102,7 +102,7 @@ nvfp4_status publish_empty(const RowCall& c, cudaStream_t s) {
 
 nvfp4::RowOutput row_output(const RowCall& c) {
   return {c.out,   c.ld_out, c.scales, c.layout == NVFP4_SF_SWIZZLED, c.format, c.gs_in, c.gs_out,
-          static_cast<uint32_t*>(c.workspace)};
+          static_cast<uint32_t*>(c.workspace), false};
 }
 
 nvfp4_status matvec(const void* x, const uint8_t* x_scales, int x_layout, int64_t M, int64_t K, int64_t ld_x,
@@ -174,7 +174,7 @@ nvfp4_status nvfp4_rms_norm(const void* x, int64_t rows, int64_t cols, int64_t l
   if (rows == 0) return publish_empty(c, s);
   const nvfp4::NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual),
                           static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(residual_out), ld_x,
-                          ld_residual, ld_residual_out, rows, cols, eps, weight_offset};
+                          ld_residual, ld_residual_out, rows, cols, eps, weight_offset, false};
   return nvfp4::launch_rms_norm(a, row_output(c), &nvfp4::g_last_launches, s) == cudaSuccess ? NVFP4_OK
                                                                                             : NVFP4_ERR_CUDA;
 }
@@ -202,7 +202,7 @@ nvfp4_status nvfp4_silu_mul(const void* gate, int64_t ld_gate, const void* up, i
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0) return publish_empty(c, s);
   const nvfp4::GateArgs a{static_cast<const uint16_t*>(gate), static_cast<const uint16_t*>(up), ld_gate, ld_up, rows,
-                          cols};
+                          cols, false};
   return nvfp4::launch_silu_mul(a, row_output(c), &nvfp4::g_last_launches, s) == cudaSuccess ? NVFP4_OK
                                                                                             : NVFP4_ERR_CUDA;
 }

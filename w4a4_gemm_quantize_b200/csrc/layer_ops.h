@@ -21,6 +21,7 @@ struct RowOutput {
   const float* gs_in;  // NVFP4: the given tensor scale, or null: computed from the output's amax
   float* gs_out;       // NVFP4: receives the tensor scale (may be null)
   uint32_t* amax_word; // NVFP4 without gs_in: one word of scratch
+  bool wide;           // (launchers) BF16 rows of out at multiples of 32 bytes
 };
 
 struct NormArgs {
@@ -31,6 +32,7 @@ struct NormArgs {
   int64_t ld_x, ld_res, ld_res_out;
   int64_t rows, cols;
   float eps, weight_offset;
+  bool wide;  // (launcher) rows of every matrix but the output at multiples of 32 bytes
 };
 
 struct GateArgs {
@@ -38,6 +40,7 @@ struct GateArgs {
   const uint16_t* up;
   int64_t ld_gate, ld_up;
   int64_t rows, cols;
+  bool wide;  // (launcher) rows of both at multiples of 32 bytes
 };
 
 // Each adds the number of kernels it enqueued to *launches.  rows, cols >= 1.

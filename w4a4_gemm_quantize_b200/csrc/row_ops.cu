@@ -13,7 +13,7 @@
 //     E2M1(v * RN(1 / (s_b s_g))), s_g given or amax / 2688 over the whole output
 //     (1 for an all-zero one).  A block that holds a NaN has a NaN scale.
 //
-// One thread owns 16 consecutive values (two 16-byte loads): an NVFP4 block, or half
+// One thread owns 16 consecutive values (a 32-byte load): an NVFP4 block, or half
 // an MX block (the pair of lanes shares its maximum with one shuffle).
 #include <cuda_runtime.h>
 
@@ -28,6 +28,9 @@ namespace {
 
 constexpr int kUnit = 16;       // values per thread step
 constexpr int kCluster = 8;     // CTAs that share one amax through distributed shared memory
+// Values of a gate that one cluster handles, amax and all, instead of a memset and two
+// launches (8.2 us): 4.1 us for 14336 or 28672, 8.4 us for 114688.
+constexpr int64_t kClusterMax = 128 * 1024;
 // Threads per row and units per thread of norm_kernel: U = 1 up to 1024 threads, U = 2,
 // 4, 8 up to 512 (64 or 128 registers each); the longest row is 8 x 512 units.
 constexpr int norm_threads(int U) { return U == 1 ? 1024 : 512; }
@@ -81,15 +84,29 @@ __device__ __forceinline__ void widen(const uint32_t (&w)[8], float (&v)[16]) {
   }
 }
 
-__device__ __forceinline__ void load_unit(const uint16_t* p, uint32_t (&w)[8]) {
-  const uint4 a = ld_v4(p), b = ld_v4(p + 8);
-  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+// A unit is one 32-byte access where every row starts at a multiple of 32 bytes (`wide`),
+// else two of 16 (8192 x 5376 to MXFP8 47.7 against 50.7 us).
+__device__ __forceinline__ void load_unit(const uint16_t* p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = ld_v4(p), b = ld_v4(p + 8);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
 }
 
-__device__ __forceinline__ void store_unit(uint16_t* p, const uint32_t (&w)[8]) {
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+__device__ __forceinline__ void store_unit(uint16_t* p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 __device__ __forceinline__ float amax16(const float (&v)[16]) {
@@ -124,7 +141,7 @@ __device__ __forceinline__ void emit(const float (&v)[16], int64_t r, int64_t u,
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    store_unit(static_cast<uint16_t*>(o.out) + r * o.ld_out + u * kUnit, w);
+    store_unit(static_cast<uint16_t*>(o.out) + r * o.ld_out + u * kUnit, o.wide, w);
   } else {
     const int lane = threadIdx.x & 31;
     constexpr int kLanes = FMT == NVFP4_OUT_NVFP4 ? 1 : 2;  // lanes per block
@@ -279,7 +296,7 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
   for (int k = 0; k < U; ++k) {
     const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
     if (row && u < units) {
-      load_unit(src + u * kUnit, h[k]);
+      load_unit(src + u * kUnit, a.wide, h[k]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[k][i] = 0u;
@@ -291,11 +308,11 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
       const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
       if (row && u < units) {
         uint32_t q[8];
-        load_unit(a.residual + r * a.ld_res + u * kUnit, q);
+        load_unit(a.residual + r * a.ld_res + u * kUnit, a.wide, q);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           h[k][i] = pack_bf16(bf16_lo(h[k][i]) + bf16_lo(q[i]), bf16_hi(h[k][i]) + bf16_hi(q[i]));
-        store_unit(a.residual_out + r * a.ld_res_out + u * kUnit, h[k]);
+        store_unit(a.residual_out + r * a.ld_res_out + u * kUnit, a.wide, h[k]);
       }
     }
   } else if (add) {  // all loads of the residual in flight together
@@ -303,7 +320,7 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
-      if (row && u < units) load_unit(a.residual + r * a.ld_res + u * kUnit, q[k]);
+      if (row && u < units) load_unit(a.residual + r * a.ld_res + u * kUnit, a.wide, q[k]);
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -312,7 +329,7 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           h[k][i] = pack_bf16(bf16_lo(h[k][i]) + bf16_lo(q[k][i]), bf16_hi(h[k][i]) + bf16_hi(q[k][i]));
-        store_unit(a.residual_out + r * a.ld_res_out + u * kUnit, h[k]);
+        store_unit(a.residual_out + r * a.ld_res_out + u * kUnit, a.wide, h[k]);
       }
     }
   }
@@ -380,55 +397,114 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
 }
 
 // BF16 rows that the 16-value units do not fit (odd sizes, strides or addresses, or rows
-// longer than a CTA's registers hold): one value per thread and step, the second pass
-// re-reads h (each thread its own values, so x may be the output).
+// longer than a CTA's registers hold): one value per thread and step.  CACHED: a thread's
+// kAny values stay in registers; else the second pass re-reads h (each thread its own
+// values, so x may be the output).
+constexpr int kAny = 8;
+template <bool CACHED>
 __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_t* out, int64_t ld_out) {
   __shared__ float sums[32];
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t r = blockIdx.x;
   const uint16_t* x = a.x + r * a.ld_x;
-  float s = 0.0f;
-  if (a.residual) {
-    const uint16_t* q = a.residual + r * a.ld_res;
-    uint16_t* ho = a.residual_out + r * a.ld_res_out;
-    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
-      const uint32_t h = pack_bf16(bf16_bits_to_float(x[c]) + bf16_bits_to_float(q[c]), 0.0f) & 0xFFFFu;
-      ho[c] = static_cast<uint16_t>(h);
-      const float f = bf16_bits_to_float(h);
-      s = __fmaf_rn(f, f, s);
-    }
-    x = ho;
-  } else {
-    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
-      const float f = bf16_bits_to_float(x[c]);
-      s = __fmaf_rn(f, f, s);
-    }
-  }
-  const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
-  for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
-    float v = __fmul_rn(bf16_bits_to_float(x[c]), rstd);
+  const uint16_t* q = a.residual ? a.residual + r * a.ld_res : nullptr;
+  uint16_t* ho = a.residual_out + r * a.ld_res_out;
+  auto value = [&](int64_t c) {  // h of column c, stored on the way
+    const float f = bf16_bits_to_float(x[c]);
+    if (q == nullptr) return f;
+    const uint32_t h = pack_bf16(f + bf16_bits_to_float(q[c]), 0.0f) & 0xFFFFu;
+    ho[c] = static_cast<uint16_t>(h);
+    return bf16_bits_to_float(h);
+  };
+  auto finish = [&](int64_t c, float f, float rstd) {
+    float v = __fmul_rn(f, rstd);
     if (a.weight) v = __fmul_rn(v, __fadd_rn(bf16_bits_to_float(a.weight[c]), a.weight_offset));
     out[r * ld_out + c] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+  };
+  float s = 0.0f;
+  if constexpr (CACHED) {
+    float f[kAny];
+#pragma unroll
+    for (int i = 0; i < kAny; ++i) {
+      const int64_t c = threadIdx.x + i * static_cast<int64_t>(blockDim.x);
+      f[i] = c < a.cols ? value(c) : 0.0f;
+      s = __fmaf_rn(f[i], f[i], s);
+    }
+    const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
+#pragma unroll
+    for (int i = 0; i < kAny; ++i) {
+      const int64_t c = threadIdx.x + i * static_cast<int64_t>(blockDim.x);
+      if (c < a.cols) finish(c, f[i], rstd);
+    }
+  } else {
+    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+      const float f = value(c);
+      s = __fmaf_rn(f, f, s);
+    }
+    const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
+    const uint16_t* h = q ? ho : x;
+    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) finish(c, bf16_bits_to_float(h[c]), rstd);
   }
 }
 
-// g / (1 + e^-g) * u.  The quotient is refined to about half a unit in the last place, so
-// that the block formats' rounding borders see no more error than a plain binary32
-// evaluation has.  Where the refinement has no meaning (1 + e^-g or g infinite) its NaN
-// gives way to the first quotient, which is the IEEE one: 0, an infinity, or NaN.
+// g / (1 + e^-g) * u of one value, by IEEE operations: the tails, infinities and NaN.
 __device__ __forceinline__ float silu_times(float g, float u) {
-  const float d = __fadd_rn(1.0f, expf(-g));
-  float rc;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(d));
-  const float q0 = __fmul_rn(g, rc);
-  const float q = __fmaf_rn(__fmaf_rn(-d, q0, g), rc, q0);
-  return __fmul_rn(q == q ? q : q0, u);
+  return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
 }
+
+// The same of the sixteen values of a unit, two to a packed instruction, for |g| < 80.
+//   e^-g = 2^h (1 + l ln 2), h = RN(-g log2 e), l what h leaves of -g log2 e, with the second
+//   word of log2 e; d = 1 + e^-g; 1 / d by the approximate reciprocal and one Newton step.
+// The error stays near one unit in the last place, so the block formats' rounding borders see
+// no more of it than a plain binary32 evaluation has.  Written out because the issue rate
+// bounds this kernel: 12 instructions a value instead of 21 took 8192 x 21504 to MXFP8 from
+// 172 us to 157.
+__device__ __forceinline__ void silu_unit(const uint32_t (&g)[8], const uint32_t (&u)[8], float (&v)[16]) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) big = __vmaxu2(big, g[i] & 0x7FFF7FFFu);
+  if (max(big & 0xFFFFu, big >> 16) >= 0x42A0u) {  // 80.0 in BF16
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = silu_times(bf16_lo(g[i]), bf16_lo(u[i]));
+      v[2 * i + 1] = silu_times(bf16_hi(g[i]), bf16_hi(u[i]));
+    }
+    return;
+  }
+  const uint64_t m_l2e = pack2(-1.44269502f, -1.44269502f);
+  const uint64_t l2e = pack2(1.44269502f, 1.44269502f);             // RN(log2 e)
+  const uint64_t l2e_lo = pack2(1.92596299e-8f, 1.92596299e-8f);    // log2 e - RN(log2 e)
+  const uint64_t ln2 = pack2(0.693147182f, 0.693147182f), m_one = pack2(-1.0f, -1.0f), one = pack2(1.0f, 1.0f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t x = pack2(bf16_lo(g[i]), bf16_hi(g[i]));
+    const uint64_t h = mul2(x, m_l2e);
+    const uint64_t ml = fma2(x, l2e_lo, fma2(x, l2e, h));  // -l: the inner one exact
+    float h0, h1, e0, e1;
+    unpack2(h, h0, h1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(h0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(h1));
+    // -d = -1 - e (1 + l ln 2), and 1 + l ln 2 = 1 - ln 2 (-l)
+    const uint64_t nd = fma2(pack2(e0, e1), fma2(ml, ln2, m_one), m_one);
+    float d0, d1, r0, r1;
+    unpack2(nd, d0, d1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-d0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-d1));
+    const uint64_t r = pack2(r0, r1);
+    const uint64_t q = mul2(mul2(x, fma2(fma2(nd, r, one), r, r)), pack2(bf16_lo(u[i]), bf16_hi(u[i])));
+    unpack2(q, v[2 * i], v[2 * i + 1]);
+  }
+}
+
+constexpr int kGateThreads = 256;
+// CTAs of gate_kernel that an SM is to hold (64 or 80 registers a thread; NVFP4's encoding at
+// 64 is 4 % slower).
+constexpr int gate_ctas(int fmt, int phase) { return fmt == NVFP4_OUT_NVFP4 && phase != kAmax ? 3 : 4; }
 
 // One warp per 32 consecutive units of a row.
 template <int FMT, int PHASE>
-__global__ void __launch_bounds__(256) gate_kernel(const GateArgs a, const RowOutput o) {
+__global__ void __launch_bounds__(kGateThreads, gate_ctas(FMT, PHASE)) gate_kernel(const GateArgs a, const RowOutput o) {
   __shared__ uint32_t maxima[32];
   __shared__ float cta_max;
   grid_dependency_wait();
@@ -451,32 +527,41 @@ __global__ void __launch_bounds__(256) gate_kernel(const GateArgs a, const RowOu
     }
   };
 
-  auto load = [&](int64_t r, int64_t u, float (&v)[16]) {
-    const bool active = u < units;
+  // The tasks' values in turn: f(r, u, active, v) for each, the next task's loads requested
+  // before f.  `back`: from the last task to the first.
+  auto each = [&](bool back, auto f) {
     uint32_t g[8], q[8];
-    if (active) {
-      load_unit(a.gate + r * a.ld_gate + u * kUnit, g);
-      load_unit(a.up + r * a.ld_up + u * kUnit, q);
-    } else {
+    auto request = [&](int64_t r, int64_t u) {
+      if (r < a.rows && u < units) {
+        if (back) r = a.rows - 1 - r;
+        load_unit(a.gate + r * a.ld_gate + u * kUnit, a.wide, g);
+        load_unit(a.up + r * a.ld_up + u * kUnit, a.wide, q);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = q[i] = 0u;
-    }
+        for (int i = 0; i < 8; ++i) g[i] = q[i] = 0u;
+      }
+    };
+    auto unit = [&](int64_t c) { return (back ? chunks - 1 - c : c) * 32 + lane; };
+    int64_t r = r0, c = c0;
+    request(r, unit(c));
+    while (r < a.rows) {
+      const int64_t row = back ? a.rows - 1 - r : r, u = unit(c);
+      float v[16];
+      uint32_t g0[8], q0[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = silu_times(bf16_lo(g[i]), bf16_lo(q[i]));
-      v[2 * i + 1] = silu_times(bf16_hi(g[i]), bf16_hi(q[i]));
+      for (int i = 0; i < 8; ++i) g0[i] = g[i], q0[i] = q[i];
+      next(r, c);
+      request(r, unit(c));
+      silu_unit(g0, q0, v);
+      f(row, u, u < units, v);
     }
-    return active;
   };
 
   float sg = 1.0f;
   if constexpr (PHASE == kCluster1 || PHASE == kAmax) {
     float m = 0.0f;
-    for (int64_t r = r0, c = c0; r < a.rows; next(r, c)) {
-      float v[16];
-      load(r, c * 32 + lane, v);  // an inactive lane's values are 0
-      m = max_nan(m, amax16(v));
-    }
+    // (an inactive lane's values are 0)
+    each(false, [&](int64_t, int64_t, bool, const float(&v)[16]) { m = max_nan(m, amax16(v)); });
     m = block_max(m, maxima);
     if constexpr (PHASE == kAmax) {
       if (threadIdx.x == 0 && __float_as_uint(m) != 0u) atomicMax(o.amax_word, __float_as_uint(m));
@@ -487,14 +572,10 @@ __global__ void __launch_bounds__(256) gate_kernel(const GateArgs a, const RowOu
     sg = PHASE == kFormat ? tensor_scale(__uint_as_float(*o.amax_word)) : *o.gs_in;
   }
   if (FMT == NVFP4_OUT_NVFP4 && o.gs_out && blockIdx.x == 0 && threadIdx.x == 0) *o.gs_out = sg;
-  for (int64_t r = r0, c = c0; r < a.rows; next(r, c)) {
-    // the second launch walks backwards: the end of the first's reads is in L2
-    const int64_t rr = PHASE == kFormat ? a.rows - 1 - r : r;
-    const int64_t u = (PHASE == kFormat ? chunks - 1 - c : c) * 32 + lane;
-    float v[16];
-    const bool active = load(rr, u, v);
-    emit<FMT>(v, rr, u, active, a.cols, sg, o);
-  }
+  // the second launch walks backwards: the end of the first's reads is in L2
+  each(PHASE == kFormat, [&](int64_t r, int64_t u, bool active, const float(&v)[16]) {
+    emit<FMT>(v, r, u, active, a.cols, sg, o);
+  });
   if (FMT != NVFP4_OUT_BF16 && o.swizzled)
     zero_row_padding(o.scales, a.rows, a.cols / (FMT == NVFP4_OUT_NVFP4 ? 16 : 32),
                      static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
@@ -544,6 +625,7 @@ cudaError_t launch(void (*kernel)(KArgs...), int64_t grid, int threads, int clus
 }
 
 bool fits_units(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+bool fits_wide(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld % 16 == 0; }
 
 template <int FMT, int PHASE>
 cudaError_t norm_launch_u(const NormArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
@@ -565,27 +647,41 @@ cudaError_t norm_launch_u(const NormArgs& a, const RowOutput& o, int* launches, 
 
 template <int FMT, int PHASE>
 cudaError_t gate_launch(const GateArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
+  constexpr int T = kGateThreads;
+  if (PHASE == kCluster1)
+    return launch(gate_kernel<FMT, PHASE>, kCluster, T, kCluster, stream, launches, a, o);
   const int64_t warps = a.rows * ((a.cols / kUnit + 31) / 32);
-  int64_t grid = PHASE == kCluster1 ? kCluster : (warps + 7) / 8;
+  int64_t grid = (warps + T / 32 - 1) / (T / 32);
+  // (a grid of resident CTAs only, each with the same work, is 2 to 4 % slower)
   const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
   if (grid > cap) grid = cap;
-  if (PHASE == kOnePass || PHASE == kFormat) {
-    const int64_t pad = (padding_lines(a.rows, a.cols, o) + 255) / 256;
+  if (PHASE != kAmax) {
+    const int64_t pad = (padding_lines(a.rows, a.cols, o) + T - 1) / T;
     if (grid < pad) grid = pad < cap ? pad : cap;
   }
-  return launch(gate_kernel<FMT, PHASE>, grid, 256, PHASE == kCluster1 ? kCluster : 1, stream, launches, a, o);
+  return launch(gate_kernel<FMT, PHASE>, grid, T, 1, stream, launches, a, o);
 }
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const NormArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
+cudaError_t launch_rms_norm(const NormArgs& args, const RowOutput& output, int* launches, cudaStream_t stream) {
+  NormArgs a = args;
+  RowOutput o = output;
+  a.wide = fits_wide(a.x, a.ld_x) &&
+           (!a.residual || (fits_wide(a.residual, a.ld_res) && fits_wide(a.residual_out, a.ld_res_out)));
+  o.wide = fits_wide(o.out, o.ld_out);
   const bool units = a.cols % kUnit == 0 && a.cols <= kNormMaxCols &&
                      fits_units(a.x, a.ld_x) && fits_units(a.weight, 0) &&
                      (!a.residual || (fits_units(a.residual, a.ld_res) && fits_units(a.residual_out, a.ld_res_out)));
   switch (o.format) {
     case NVFP4_OUT_BF16:
       if (units && fits_units(o.out, o.ld_out)) return norm_launch_u<NVFP4_OUT_BF16, kOnePass>(a, o, launches, stream);
-      return launch(norm_any_kernel, a.rows, 512, 1, stream, launches, a, static_cast<uint16_t*>(o.out), o.ld_out);
+      if (a.cols <= 512 * kAny) {
+        const int T = static_cast<int>(((a.cols + kAny - 1) / kAny + 31) / 32 * 32);
+        return launch(norm_any_kernel<true>, a.rows, T, 1, stream, launches, a, static_cast<uint16_t*>(o.out), o.ld_out);
+      }
+      return launch(norm_any_kernel<false>, a.rows, 512, 1, stream, launches, a, static_cast<uint16_t*>(o.out),
+                    o.ld_out);
     case NVFP4_OUT_MXFP8: return norm_launch_u<NVFP4_OUT_MXFP8, kOnePass>(a, o, launches, stream);
     case NVFP4_OUT_MXFP4: return norm_launch_u<NVFP4_OUT_MXFP4, kOnePass>(a, o, launches, stream);
     default: break;
@@ -598,7 +694,11 @@ cudaError_t launch_rms_norm(const NormArgs& a, const RowOutput& o, int* launches
   return e;
 }
 
-cudaError_t launch_silu_mul(const GateArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
+cudaError_t launch_silu_mul(const GateArgs& args, const RowOutput& output, int* launches, cudaStream_t stream) {
+  GateArgs a = args;
+  RowOutput o = output;
+  a.wide = fits_wide(a.gate, a.ld_gate) && fits_wide(a.up, a.ld_up);
+  o.wide = fits_wide(o.out, o.ld_out);
   switch (o.format) {
     case NVFP4_OUT_BF16: {
       if (a.cols % kUnit == 0 && fits_units(a.gate, a.ld_gate) && fits_units(a.up, a.ld_up) &&
@@ -615,7 +715,7 @@ cudaError_t launch_silu_mul(const GateArgs& a, const RowOutput& o, int* launches
   }
   if (o.gs_in) return gate_launch<NVFP4_OUT_NVFP4, kOnePass>(a, o, launches, stream);
   // a small output: one cluster computes the amax and formats
-  if (a.rows * a.cols <= 256 * 1024) return gate_launch<NVFP4_OUT_NVFP4, kCluster1>(a, o, launches, stream);
+  if (a.rows * a.cols <= kClusterMax) return gate_launch<NVFP4_OUT_NVFP4, kCluster1>(a, o, launches, stream);
   cudaError_t e = cudaMemsetAsync(o.amax_word, 0, sizeof(uint32_t), stream);
   if (e == cudaSuccess) e = gate_launch<NVFP4_OUT_NVFP4, kAmax>(a, o, launches, stream);
   if (e == cudaSuccess) e = gate_launch<NVFP4_OUT_NVFP4, kFormat>(a, o, launches, stream);
