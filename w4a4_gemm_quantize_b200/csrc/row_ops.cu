@@ -183,7 +183,7 @@ __device__ __forceinline__ void emit(const float (&v)[16], int64_t r, int64_t u,
       }
     }
     const int64_t b = u / kLanes;
-    if (o.swizzled) {
+    if (o.swizzled || (nblk & 3) == 0) {
       // four consecutive blocks' bytes in one 32-bit store; a block past the row's end
       // is the tile's padding and contributes 0
       if (!active) sbyte = 0;
@@ -192,7 +192,8 @@ __device__ __forceinline__ void emit(const float (&v)[16], int64_t r, int64_t u,
       const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, sbyte, 3 * kLanes);
       if (active && (lane % (4 * kLanes)) == 0) {
         const int64_t atoms = (nblk + 3) / 4;
-        const int64_t at = ((r >> 7) * atoms + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+        const int64_t at = o.swizzled ? ((r >> 7) * atoms + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4
+                                      : r * nblk + b;
         *reinterpret_cast<uint32_t*>(o.scales + at) = sbyte | (s1 << 8) | (s2 << 16) | (s3 << 24);
       }
     } else if (active && (lane % kLanes) == 0) {
