@@ -304,7 +304,8 @@ size_t nvfp4_row_workspace_bytes(void);
  *   h = BF16(x + residual)  (h = x without a residual), stored to residual_out;
  *   v = (h r) (weight + weight_offset),  r = 1 / sqrt(mean over the row of h^2 + eps),
  * sums and v in FP32.  The norm sees the rounded h, the value that the residual stream
- * keeps, so the call equals an addition in BF16 followed by a norm.
+ * keeps, so the call equals an addition in BF16 followed by a norm.  (A row whose mean
+ * square overflows FP32 becomes 0; one with a NaN or an infinity follows the formula.)
  *   x            device, BF16, rows x cols, row stride ld_x.
  *   residual     device, BF16, rows x cols, row stride ld_residual, or NULL.
  *   residual_out device, BF16, rows x cols, row stride ld_residual_out; NULL exactly when
@@ -350,7 +351,8 @@ nvfp4_status nvfp4_silu_mul(const void *gate, int64_t ld_gate, const void *up, i
  *                SWIZZLED).
  *   gate_codes, gate_scales, gate_global_scale  NULL, or a second N x K weight G:
  *                y = silu(x G^T) * (x W^T), both products unrounded in FP32.
- *   out          device BF16, M x N, row stride ld_out >= N (2-byte aligned, any stride).
+ *   out          device BF16, M x N, row stride ld_out >= N (2-byte aligned, any stride);
+ *                it must not overlap an input (INVALID_ARG).
  *   0 <= M <= 16, 1 <= N <= 2^30, 32 <= K <= 2^19, K % 32 == 0.
  * FP32 accumulation, no workspace, the same bits on every call.  Weights are exact; x is
  * exact down to 2^-21 of the largest finite magnitude of its token (in the part of K that

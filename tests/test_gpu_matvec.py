@@ -77,6 +77,59 @@ def test_matvec_gated(cuda_device, M, N, K, kind):
     ref.check_product(nv.matvec(x8, w, g), y, bound, f"gated {kind} mxfp8 {M}x{N}x{K}", min_exact=0.85)
 
 
+def test_matvec_on_many_shapes(cuda_device):
+    """Sizes drawn over the whole range: every split of K over a cluster, tiles and chunks that end anywhere."""
+    r = np.random.default_rng(7)
+    for i in range(60):
+        M, K = int(r.integers(1, 17)), 32 * int(np.exp(r.uniform(0, np.log(700))))
+        N = int(np.exp(r.uniform(0, np.log(min(6000, 4e7 / K)))))
+        kind, gated, fp8 = ("nvfp4", "mxfp4")[i % 2], r.random() < 0.3, r.random() < 0.4
+        x = bf16((M, K), i)
+        x = mxfp8(x, ("linear", "swizzled")[i // 2 % 2]) if fp8 else x
+        w, g = weight(N, K, kind, i), weight(N, K, kind, i + 100) if gated else None
+        y, bound = ref.matvec64(values(x), w, g)
+        ref.check_product(nv.matvec(x, w, g), y, bound, f"{kind} {M}x{N}x{K} gated={gated} fp8={fp8}", 0.85)
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "mxfp4"])
+def test_matvec_past_two_to_the_31_bytes_of_codes(cuda_device, kind):
+    """A weight whose last rows lie more than 2^31 bytes behind its first: random codes, sampled rows checked."""
+    N, K, M = 140_000, 32768, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    block = 16 if kind == "nvfp4" else 32
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    n = (N + 127) // 128 * 128 * (K // block)
+    low, high = (0x30, 0x48) if kind == "nvfp4" else (118, 126)
+    scales = torch.randint(low, high, (n,), generator=g, device="cuda", dtype=torch.uint8)
+    if kind == "nvfp4":
+        w = nv.NVFP4Tensor(codes, scales, torch.tensor([0.01], device="cuda"), N, K)
+    else:
+        w = nv.MXFP4Tensor(codes, scales, N, K)
+    x = bf16((M, K), 1)
+    got = nv.matvec(x, w)
+    group = slice((N // 128) * 128, N)                       # the last rows, and rows of two groups on the way
+    for rows in (slice(0, 128), slice(65536, 65536 + 128), group):
+        a, b = rows.start, rows.stop
+        per_group = 128 * (K // block)
+        part = scales[a // 128 * per_group: (b + 127) // 128 * per_group]
+        sub = (nv.NVFP4Tensor(codes[a:b], part, w.global_scale, b - a, K) if kind == "nvfp4"
+               else nv.MXFP4Tensor(codes[a:b], part, b - a, K))
+        m = torch.from_numpy(dequantize_any(sub)).cuda()
+        y = x.double() @ m.t()
+        S = (x.double().abs() @ m.abs().t()) * 2.0 ** -14
+        ref.check_product(got[:, a:b], y.cpu().numpy(), S.cpu().numpy(), f"rows {a}..{b}")
+
+
+def dequantize_any(w):
+    """ref.dequantize64 without its look at the scales' padding (which is random here)."""
+    import oracle
+    block = 16 if isinstance(w, nv.NVFP4Tensor) else 32
+    s = oracle.unswizzle_scales(w.scales.cpu().numpy(), w.rows, w.cols // block)
+    eff = ref.e4m3_values(s) * float(w.global_scale.item()) if block == 16 else 2.0 ** (s.astype(np.float64) - 127)
+    v = ref.code_values(w, "fp4").reshape(w.rows, -1, block)
+    return (v * eff[..., None]).reshape(w.rows, w.cols)
+
+
 @pytest.mark.parametrize("kind", ["nvfp4", "mxfp4"])
 def test_matvec_strides_and_margins(cuda_device, kind):
     """x a column slice, y a column slice of odd stride: nothing beside them is read into it or written."""
@@ -170,7 +223,11 @@ def test_matvec_empty_batch_and_refusals(cuda_device):
                  lambda: nv.matvec(x, w, m), lambda: nv.matvec(x, w, weight(32, 96, "nvfp4", 1)),
                  lambda: nv.matvec(x, x), lambda: nv.matvec(x, w, out=torch.empty((2, 63), dtype=torch.bfloat16,
                                                                                   device="cuda")),
-                 lambda: nv.matvec(nv.MXFP8Tensor(x, x, 2, 96), w)):
+                 lambda: nv.matvec(nv.MXFP8Tensor(x, x, 2, 96), w),
+                 lambda: nv.matvec(x, nv.NVFP4Tensor(w.codes[:32], w.scales, w.global_scale, 64, 96)),
+                 lambda: nv.matvec(x, nv.NVFP4Tensor(w.codes, w.scales[:-4], w.global_scale, 64, 96)),
+                 lambda: nv.matvec(x, nv.NVFP4Tensor(w.codes, w.scales.cpu(), w.global_scale, 64, 96)),
+                 lambda: nv.matvec(x, nv.NVFP4Tensor(w.codes, w.scales, w.global_scale.cpu(), 64, 96))):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: nv.matvec(bf16((17, 96), 1), w), lambda: nv.matvec(bf16((2, 100), 1)[:, :96], w),

@@ -327,3 +327,48 @@ def test_on_another_stream(cuda_device):
         q = nv.rms_norm(x, out_format="nvfp4")
     side.synchronize()
     assert torch.equal(q.codes, want.codes)
+
+
+@pytest.mark.parametrize("op", ["norm", "gate"])
+def test_past_two_to_the_31_elements(cuda_device, op):
+    """Rows whose element offsets pass 32 bits, in BF16 and in NVFP4 under a computed tensor scale: the first and last
+    rows equal the same rows computed alone."""
+    rows, cols = 66_000, 32768
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x.view(-1).view(torch.int16).random_(0x3C00, 0x4000)              # BF16 magnitudes of 2^-7 to 2
+    if op == "norm":
+        def call(t, **k):
+            return nv.rms_norm(t, **k)
+    else:
+        def call(t, **k):
+            return nv.silu_mul(t, t, **k)
+    parts = (slice(0, 3), slice(65536, 65539), slice(rows - 3, rows))
+    out = call(x)
+    for p in parts:
+        assert torch.equal(out[p], call(x[p].clone()))
+    del out
+    q = call(x, out_format="nvfp4", layout="linear")
+    for p in parts:
+        alone = call(x[p].clone(), out_format="nvfp4", layout="linear", global_scale=q.global_scale)
+        assert torch.equal(q.codes[p], alone.codes) and torch.equal(q.scales[p], alone.scales)
+
+
+def test_rows_and_formats_drawn_at_random(cuda_device):
+    """Sizes drawn over the whole range, odd ones among them, each format and operator."""
+    r = np.random.default_rng(11)
+    for i in range(80):
+        fmt = FORMATS[i % 4]
+        step = {"bf16": 1, "nvfp4": 16}.get(fmt, 32)
+        cols = step * int(np.exp(r.uniform(0, np.log(12000 / step))))
+        rows = int(np.exp(r.uniform(0, np.log(2e6 / cols))))
+        layout = ("swizzled", "linear")[i // 4 % 2]
+        x, y = bf16((rows, cols), i, 2.0), bf16((rows, cols), i + 1000)
+        if r.random() < 0.5:
+            w = bf16((1, cols), 5).view(-1)
+            q, h = nv.rms_norm(x, w, y, out_format=fmt, layout=layout)
+            v, h64 = ref.norm64(x, y, w, 1e-6)
+            assert np.array_equal(h.double().cpu().numpy(), h64)
+            delta = ref.NORM_DELTA
+        else:
+            q, v, delta = nv.silu_mul(x, y, out_format=fmt, layout=layout), ref.gate64(x, y), ref.GATE_DELTA
+        check(q, v, fmt, layout, delta, where=f"{fmt} {rows}x{cols}")

@@ -131,6 +131,8 @@ def test_matvec_validation(lib, mx):
     assert mv(gc=6 << 20) == 1 and mv(gsc=6 << 20) == 1
     assert mv(gc=6 << 20, gsc=7 << 20, ggs=8 << 20) in NO_DEVICE
     assert mv(out=1 << 20) == 1                                        # over x
+    assert mv(out=2 << 20) == 1 and mv(out=(3 << 20) + 2) == 1         # over the weight's codes, its scales
+    assert mv(gc=6 << 20, gsc=7 << 20, ggs=8 << 20, out=7 << 20) == 1  # over the gate's scales
     if not mx:
         assert mv(gs=0) == 1 and mv(gs=(4 << 20) + 2) == 3
         assert mv(gc=6 << 20, gsc=7 << 20) == 1                        # the gate's tensor scale is missing

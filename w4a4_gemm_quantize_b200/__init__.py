@@ -568,9 +568,15 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
     if not nvfp4 and not isinstance(w, MXFP4Tensor):
         raise ValueError("w must be an NVFP4Tensor or an MXFP4Tensor")
     N, dev = w.rows, data.get_device()
+    codes_n, scales_n = N * (K // 2), _swizzled_bytes(N, K // (16 if nvfp4 else 32))
     for t in (w,) if w_gate is None else (w, w_gate):
-        if type(t) is not type(w) or t.rows != N or t.cols != K or t.layout != SF_SWIZZLED or t.codes.get_device() != dev:
-            raise ValueError("the weights must share K with x, one kind and shape, x's device, and have swizzled scales")
+        if type(t) is not type(w) or t.rows != N or t.cols != K or t.layout != SF_SWIZZLED:
+            raise ValueError("the weights must share K with x, one kind and shape, and have swizzled scales")
+        c, s = t.codes, t.scales
+        if c.get_device() != dev or s.get_device() != dev or (nvfp4 and t.global_scale.get_device() != dev):
+            raise ValueError(f"the weights must be on {data.device}")
+        if c.numel() != codes_n or s.numel() != scales_n or not c.is_contiguous() or not s.is_contiguous():
+            raise ValueError(f"a weight's codes or scales are not those of a {N} x {K} tensor")
     if _elsewhere(data, stream):
         with _On(data.device, stream):
             return matvec(x, w, w_gate, out)

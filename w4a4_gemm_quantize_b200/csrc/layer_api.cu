@@ -120,14 +120,19 @@ nvfp4_status matvec(const void* x, const uint8_t* x_scales, int x_layout, int64_
       !aligned(gate.gs, 4) || !aligned(out, 2))
     return NVFP4_ERR_ALIGNMENT;
   const Region o{out, M, N, ld_out, 2};
-  if (overlap(o, {x, M, K, ld_x, x_scales ? 1 : 2})) return NVFP4_ERR_INVALID_ARG;
+  const int64_t codes = N * (K / 2), scales = (N + 127) / 128 * 128 * ((K / (mx ? 32 : 16) + 3) / 4 * 4);
+  if (overlap(o, {x, M, K, ld_x, x_scales ? 1 : 2}) || overlap(o, {x_scales, 1, M * (K / 32), M * (K / 32), 1}))
+    return NVFP4_ERR_INVALID_ARG;
+  for (const nvfp4::Weight4& t : {w, gate})
+    if (overlap(o, {t.codes, 1, codes, codes, 1}) || overlap(o, {t.scales, 1, scales, scales, 1}))
+      return NVFP4_ERR_INVALID_ARG;
   const nvfp4_status st = nvfp4_check_device();
   if (st != NVFP4_OK || M == 0) return st;
   const nvfp4::MatvecArgs a{x,  x_scales, x_layout == NVFP4_SF_SWIZZLED, ld_x, w, gate, mx, static_cast<int>(M), N, K,
                             static_cast<uint16_t*>(out), ld_out};
-  if (nvfp4::launch_matvec(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return NVFP4_ERR_CUDA;
-  ++nvfp4::g_last_launches;
-  return NVFP4_OK;
+  return nvfp4::launch_matvec(a, &nvfp4::g_last_launches, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
 }
 
 }  // namespace

@@ -69,6 +69,7 @@ struct MatvecArgs {
 
 constexpr int kMatvecMaxTokens = 16;
 
-cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream);
+// One launch, or several when x of so many tokens does not fit shared memory.
+cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t stream);
 
 }  // namespace nvfp4

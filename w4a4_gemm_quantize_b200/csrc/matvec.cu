@@ -772,7 +772,7 @@ Plan plan(int M, int x_units, int tiles, int split, size_t ring, int R) {
 
 }  // namespace
 
-cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
+cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t stream) {
   Params p{};
   p.a = a;
   const bool gated = a.gate.codes != nullptr;
@@ -819,13 +819,14 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
     // (an MXFP8 scale row: 16 bytes further in the 128 x 4 tiles, K / 32 bytes in rows)
     if (a.x_scales) second.x_scales = a.x_scales + first.M * (a.x_swizzled ? 16 : a.K / 32);
     second.out = a.out + first.M * a.ld_out;
-    const cudaError_t e = launch_matvec(first, stream);
-    return e != cudaSuccess ? e : launch_matvec(second, stream);
+    const cudaError_t e = launch_matvec(first, launches, stream);
+    return e != cudaSuccess ? e : launch_matvec(second, launches, stream);
   }
   p.m_inv = static_cast<uint32_t>(((uint64_t{1} << 32) + a.M - 1) / a.M);
   p.tiles_q = p.tiles / groups, p.tiles_r = p.tiles % groups;
   p.units_q = p.units / p.split, p.units_r = p.units % p.split;
   const int grid = groups * p.split;
+  ++*launches;
   if (a.mx) return gated ? launch_format<true, true>(p, shape, grid, smem, stream)
                          : launch_format<true, false>(p, shape, grid, smem, stream);
   return gated ? launch_format<false, true>(p, shape, grid, smem, stream)
