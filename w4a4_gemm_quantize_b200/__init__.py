@@ -202,7 +202,7 @@ def nvfp4_dequantize(q: NVFP4Tensor, out: Optional[torch.Tensor] = None, stream=
     """BF16 reconstruction q * s_b * s_g of a quantized tensor."""
     lib = load_library()
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=torch.bfloat16, device=q.codes.device)
+        out = torch.empty(q.rows, q.cols, dtype=torch.bfloat16, device=q.codes.device)
     st = lib.nvfp4_dequantize(_ptr(q.codes), _ptr(q.scales), q.layout, _ptr(q.global_scale), q.rows, q.cols,
                               _ptr(out), out.stride(0), _stream(stream))
     _check(st, "nvfp4_dequantize")
@@ -336,7 +336,7 @@ def mxfp4_quantize(x: torch.Tensor, layout="swizzled", out: Optional[MXFP4Tensor
 def mxfp4_dequantize(q: MXFP4Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     lib = load_library()
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=torch.bfloat16, device=q.codes.device)
+        out = torch.empty(q.rows, q.cols, dtype=torch.bfloat16, device=q.codes.device)
     _check(lib.mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), q.layout, q.rows, q.cols, _ptr(out), out.stride(0),
                                 _stream(stream)), "mxfp4_dequantize")
     return out
@@ -392,22 +392,22 @@ class _On:
             c.__exit__(*exc)
 
 
-def _elsewhere(x, stream) -> bool:
-    """Whether a call on x has to leave the current device or stream."""
-    return stream is not None or x.get_device() != torch._C._cuda_getDevice()
+# what torch.cuda.current_device and current_stream ask, without their host time (a few microseconds a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _ld(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None) -> int:
-    """Checks a BF16 matrix argument (of `shape`, on `like`'s device) and returns its row stride (a single row's is
-    its length, rounded up)."""
+def _ld(t: torch.Tensor, name: str, shape=None, dev: int = -1) -> int:
+    """Checks a BF16 matrix argument (of `shape`, on device `dev`) and returns its row stride (a single row's is its
+    length, rounded up)."""
     own = t.shape
     if t.dtype is not torch.bfloat16 or len(own) != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D bfloat16 CUDA tensor")
     if shape is not None:
         if own != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(own)}")
-        if t.get_device() != like.get_device():
-            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     rows, cols = own
     ld, step = t.stride()
     if step != 1 and cols > 1:
@@ -425,18 +425,9 @@ def _swizzled_bytes(rows: int, blocks: int) -> int:
     return (rows + 127) // 128 * 128 * ((blocks + 3) // 4 * 4)
 
 
-def _row_output(fmt: int, layout: int, x: torch.Tensor, out, global_scale):
-    """The output of a row operator on x's shape: (what the caller gets, data, row stride, scales, tensor scale)."""
-    rows, cols = shape = x.shape
-    if global_scale is not None:
-        if fmt != OUT_NVFP4:
-            raise ValueError("global_scale is NVFP4's tensor scale; this format has none")
-        _like(global_scale, "global_scale", torch.float32, 1, x)
-    if fmt == OUT_BF16:
-        if out is None:
-            out = torch.empty(rows, cols, dtype=torch.bfloat16, device=x.device)
-            return out, out, cols if rows > 1 else -(-cols // 16) * 16, None, None
-        return out, out, _ld(out, "out", shape, x), None, None
+def _block_output(fmt: int, layout: int, x: torch.Tensor, out, global_scale):
+    """The block-format output of a row operator on x's shape: (tensor object, codes, scales, tensor scale)."""
+    rows, cols = x.shape
     block = 16 if fmt == OUT_NVFP4 else 32
     blocks = cols // block
     if blocks * block != cols:
@@ -453,35 +444,52 @@ def _row_output(fmt: int, layout: int, x: torch.Tensor, out, global_scale):
         else:
             scales = torch.empty(_swizzled_bytes(rows, blocks), dtype=torch.uint8, device=dev)
         if fmt != OUT_NVFP4:
-            return kind(codes, scales, rows, cols, layout), codes, cols, scales, None
+            return kind(codes, scales, rows, cols, layout), codes, scales, None
         gs = torch.empty(1, dtype=torch.float32, device=dev)
-        return NVFP4Tensor(codes, scales, gs, rows, cols, layout), codes, cols, scales, gs
+        return NVFP4Tensor(codes, scales, gs, rows, cols, layout), codes, scales, gs
     if not isinstance(out, kind) or (out.rows, out.cols, out.layout) != (rows, cols, layout):
         raise ValueError(f"out must be a {kind.__name__} of {rows} x {cols} with the asked scale layout")
     _like(out.codes, "out.codes", dtype, rows * width, x)
     _like(out.scales, "out.scales", torch.uint8,
           rows * blocks if layout == SF_LINEAR else _swizzled_bytes(rows, blocks), x)
     if fmt != OUT_NVFP4:
-        return out, out.codes, cols, out.scales, None
+        return out, out.codes, out.scales, None
     _like(out.global_scale, "out.global_scale", torch.float32, 1, x)
-    return out, out.codes, cols, out.scales, out.global_scale
+    return out, out.codes, out.scales, out.global_scale
 
 
-def _row_workspace(fmt: int, global_scale, workspace, x):
-    """(workspace, its bytes): only NVFP4 with a computed tensor scale needs one."""
+def _output(fmt: int, layout: int, x: torch.Tensor, dev: int, out, global_scale, workspace):
+    """Output and workspace of a row operator on x: (what the caller gets; the addresses and sizes that the C call
+    takes: data, row stride, scales, tensor scale in and out; the workspace, to be held until the call is made)."""
+    rows, cols = x.shape
+    if fmt == OUT_BF16:
+        if global_scale is not None:
+            raise ValueError("global_scale is NVFP4's tensor scale; this format has none")
+        if out is None:
+            out = torch.empty(rows, cols, dtype=torch.bfloat16, device=x.device)
+            return out, out.data_ptr(), cols if rows > 1 else -(-cols // 16) * 16, None, None, None, None
+        return out, out.data_ptr(), _ld(out, "out", x.shape, dev), None, None, None, None
+    result, codes, scales, gs = _block_output(fmt, layout, x, out, global_scale)
+    if fmt != OUT_NVFP4:
+        if global_scale is not None:
+            raise ValueError("global_scale is NVFP4's tensor scale; this format has none")
+        return result, codes.data_ptr(), cols, scales.data_ptr(), None, None, None
+    if global_scale is not None:
+        _like(global_scale, "global_scale", torch.float32, 1, x)
+        return result, codes.data_ptr(), cols, scales.data_ptr(), global_scale.data_ptr(), gs.data_ptr(), None
     if workspace is None:
-        if fmt != OUT_NVFP4 or global_scale is not None:
-            return None, 0
-        return torch.empty(256, dtype=torch.uint8, device=x.device), 256
-    if workspace.device != x.device or not workspace.is_contiguous():
+        workspace = torch.empty(256, dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {x.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return result, codes.data_ptr(), cols, scales.data_ptr(), None, gs.data_ptr(), workspace
 
 
-def _choice(table, value, name):
-    if isinstance(value, (str, int)) and value in table:
-        return table[value]
-    raise ValueError(f"{name} must be one of {[k for k in table if isinstance(k, str)]}, got {value!r}")
+def _choices(out_format, layout):
+    try:
+        return _FORMATS[out_format], _LAYOUTS[layout]
+    except (KeyError, TypeError):
+        raise ValueError(f"out_format must be one of {list(_FORMATS)}, layout 'swizzled' or 'linear'; got "
+                         f"{out_format!r}, {layout!r}") from None
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -496,31 +504,34 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     out_format: "bf16" -> a tensor, "mxfp8" -> MXFP8Tensor, "mxfp4" -> MXFP4Tensor, "nvfp4" -> NVFP4Tensor, whose
     tensor scale is `global_scale` (a device float) or computed from v.  Returns the output, or with a residual
     (output, h); residual_out may be `residual` itself to update the stream in place."""
-    fmt, lay = _choice(_FORMATS, out_format, "out_format"), _choice(_LAYOUTS, layout, "layout")
+    fmt, lay = _choices(out_format, layout)
     ld_x = _ld(x, "x")
-    if _elsewhere(x, stream):
+    dev = x.get_device()
+    if stream is not None or dev != _current_device():
         with _On(x.device, stream):
             return rms_norm(x, weight, residual, eps, weight_offset, out_format, layout, global_scale, out,
                             residual_out, workspace)
     shape = rows, cols = x.shape
-    result, data, ld_out, scales, gs = _row_output(fmt, lay, x, out, global_scale)
+    result, data, ld_out, scales, gs_in, gs_out, ws = _output(fmt, lay, x, dev, out, global_scale, workspace)
+    w = None
     if weight is not None:
         _like(weight, "weight", torch.bfloat16, cols, x)
+        w = weight.data_ptr()
+    r = ro = None
     ld_r = ld_ro = 0
     if residual is not None:
-        ld_r = _ld(residual, "residual", shape, x)
+        ld_r, r = _ld(residual, "residual", shape, dev), residual.data_ptr()
         if residual_out is None:
             residual_out = torch.empty(rows, cols, dtype=torch.bfloat16, device=x.device)
-            ld_ro = cols if rows > 1 else ld_r
+            ld_ro = cols if rows > 1 else ld_x
         else:
-            ld_ro = _ld(residual_out, "residual_out", shape, x)
+            ld_ro = _ld(residual_out, "residual_out", shape, dev)
+        ro = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, x)
-    st = load_library().nvfp4_rms_norm(x.data_ptr(), rows, cols, ld_x, _ptr(residual), ld_r, _ptr(residual_out), ld_ro,
-                                       _ptr(weight), weight_offset, eps, fmt, lay, _ptr(global_scale),
-                                       data.data_ptr(), ld_out, _ptr(scales), _ptr(gs), _ptr(workspace), ws_bytes,
-                                       _stream(None))
+    st = (_lib or load_library()).nvfp4_rms_norm(x.data_ptr(), rows, cols, ld_x, r, ld_r, ro, ld_ro, w, weight_offset,
+                                                 eps, fmt, lay, gs_in, data, ld_out, scales, gs_out, _ptr(ws),
+                                                 0 if ws is None else ws.nbytes, _current_stream(dev))
     if st:
         _check(st, "nvfp4_rms_norm")
     return result if residual is None else (result, residual_out)
@@ -531,18 +542,18 @@ def silu_mul(gate: torch.Tensor, up: torch.Tensor, out_format: str = "bf16", lay
              stream=None):
     """silu(gate) * up of two 2-D BF16 tensors (strided views, such as the halves of one product, are fine), written
     as `out_format` like rms_norm's output (see nvfp4_silu_mul in include/nvfp4.h)."""
-    fmt, lay = _choice(_FORMATS, out_format, "out_format"), _choice(_LAYOUTS, layout, "layout")
+    fmt, lay = _choices(out_format, layout)
     ld_g = _ld(gate, "gate")
-    if _elsewhere(gate, stream):
+    dev = gate.get_device()
+    if stream is not None or dev != _current_device():
         with _On(gate.device, stream):
             return silu_mul(gate, up, out_format, layout, global_scale, out, workspace)
     rows, cols = gate.shape
-    ld_u = _ld(up, "up", gate.shape, gate)
-    result, data, ld_out, scales, gs = _row_output(fmt, lay, gate, out, global_scale)
-    workspace, ws_bytes = _row_workspace(fmt, global_scale, workspace, gate)
-    st = load_library().nvfp4_silu_mul(gate.data_ptr(), ld_g, up.data_ptr(), ld_u, rows, cols, fmt, lay,
-                                       _ptr(global_scale), data.data_ptr(), ld_out, _ptr(scales), _ptr(gs),
-                                       _ptr(workspace), ws_bytes, _stream(None))
+    ld_u = _ld(up, "up", gate.shape, dev)
+    result, data, ld_out, scales, gs_in, gs_out, ws = _output(fmt, lay, gate, dev, out, global_scale, workspace)
+    st = (_lib or load_library()).nvfp4_silu_mul(gate.data_ptr(), ld_g, up.data_ptr(), ld_u, rows, cols, fmt, lay,
+                                                 gs_in, data, ld_out, scales, gs_out, _ptr(ws),
+                                                 0 if ws is None else ws.nbytes, _current_stream(dev))
     if st:
         _check(st, "nvfp4_silu_mul")
     return result
@@ -560,7 +571,9 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
         if not isinstance(x, MXFP8Tensor) or not x.codes.is_cuda:
             raise ValueError("x must be a 2-D bfloat16 CUDA tensor or an MXFP8Tensor on a CUDA device")
         data, scales, M, K = x.codes, x.scales, x.rows, x.cols
-        ld_x, x_lay = K, _choice(_LAYOUTS, x.layout, "x.layout")
+        if x.layout not in (SF_SWIZZLED, SF_LINEAR):
+            raise ValueError(f"unknown scale layout {x.layout!r}")
+        ld_x, x_lay = K, x.layout
         _like(data, "x.codes", torch.float8_e4m3fn, M * K, data)
         _like(scales, "x.scales", torch.uint8,
               M * (K // 32) if x_lay == SF_LINEAR else _swizzled_bytes(M, K // 32), data)
@@ -577,23 +590,24 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
             raise ValueError(f"the weights must be on {data.device}")
         if c.numel() != codes_n or s.numel() != scales_n or not c.is_contiguous() or not s.is_contiguous():
             raise ValueError(f"a weight's codes or scales are not those of a {N} x {K} tensor")
-    if _elsewhere(data, stream):
+    if stream is not None or dev != _current_device():
         with _On(data.device, stream):
             return matvec(x, w, w_gate, out)
     if out is None:
         out = torch.empty(M, N, dtype=torch.bfloat16, device=data.device)
         ld_out = N
     else:
-        ld_out = max(_ld(out, "out", (M, N), data), N)
+        ld_out = max(_ld(out, "out", (M, N), dev), N)
     gc, gsc = (None, None) if w_gate is None else (w_gate.codes.data_ptr(), w_gate.scales.data_ptr())
     if nvfp4:
-        st = load_library().nvfp4_matvec(data.data_ptr(), _ptr(scales), x_lay, M, K, ld_x, w.codes.data_ptr(),
-                                         w.scales.data_ptr(), w.global_scale.data_ptr(), gc, gsc,
-                                         None if w_gate is None else w_gate.global_scale.data_ptr(), N,
-                                         out.data_ptr(), ld_out, _stream(None))
+        st = (_lib or load_library()).nvfp4_matvec(data.data_ptr(), _ptr(scales), x_lay, M, K, ld_x,
+                                                   w.codes.data_ptr(), w.scales.data_ptr(), w.global_scale.data_ptr(),
+                                                   gc, gsc, None if w_gate is None else w_gate.global_scale.data_ptr(),
+                                                   N, out.data_ptr(), ld_out, _current_stream(dev))
     else:
-        st = load_library().mxfp4_matvec(data.data_ptr(), _ptr(scales), x_lay, M, K, ld_x, w.codes.data_ptr(),
-                                         w.scales.data_ptr(), gc, gsc, N, out.data_ptr(), ld_out, _stream(None))
+        st = (_lib or load_library()).mxfp4_matvec(data.data_ptr(), _ptr(scales), x_lay, M, K, ld_x,
+                                                   w.codes.data_ptr(), w.scales.data_ptr(), gc, gsc, N,
+                                                   out.data_ptr(), ld_out, _current_stream(dev))
     if st:
         _check(st, "nvfp4_matvec" if nvfp4 else "mxfp4_matvec")
     return out
