@@ -92,6 +92,17 @@ def test_matvec_on_many_shapes(cuda_device):
 
 
 @pytest.mark.parametrize("kind", ["nvfp4", "mxfp4"])
+def test_matvec_long_rows_token_by_token(cuda_device, kind):
+    """Rows so long that x is handled a few tokens at a time, its scale rows at odd offsets."""
+    M, N, K = 3, 40, 2 ** 19 - 32
+    w = weight(N, K, kind, 1)
+    for x in (bf16((M, K), 2), mxfp8(bf16((M, K), 2)), mxfp8(bf16((M, K), 2), "swizzled")):
+        y, bound = ref.matvec64(values(x), w)
+        ref.check_product(nv.matvec(x, w), y, bound, f"{kind} {M}x{N}x{K}")
+        assert nv.last_launch_count() == 3
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "mxfp4"])
 def test_matvec_past_two_to_the_31_bytes_of_codes(cuda_device, kind):
     """A weight whose last rows lie more than 2^31 bytes behind its first: random codes, sampled rows checked."""
     N, K, M = 140_000, 32768, 3

@@ -128,8 +128,8 @@ nvfp4_status matvec(const void* x, const uint8_t* x_scales, int x_layout, int64_
       return NVFP4_ERR_INVALID_ARG;
   const nvfp4_status st = nvfp4_check_device();
   if (st != NVFP4_OK || M == 0) return st;
-  const nvfp4::MatvecArgs a{x,  x_scales, x_layout == NVFP4_SF_SWIZZLED, ld_x, w, gate, mx, static_cast<int>(M), N, K,
-                            static_cast<uint16_t*>(out), ld_out};
+  const nvfp4::MatvecArgs a{x,    x_scales, x_layout == NVFP4_SF_SWIZZLED, 0, static_cast<int>(M), ld_x, w, gate, mx,
+                            static_cast<int>(M), N, K, static_cast<uint16_t*>(out), ld_out};
   return nvfp4::launch_matvec(a, &nvfp4::g_last_launches, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? NVFP4_OK
              : NVFP4_ERR_CUDA;

@@ -58,6 +58,7 @@ struct MatvecArgs {
   const void* x;            // BF16, or E4M3 codes when x_scales is not null
   const uint8_t* x_scales;  // null, or one E8M0 byte per 32 values
   bool x_swizzled;
+  int x_row0, x_rows;       // x_scales: the row of token 0, and the rows of the whole buffer
   int64_t ld_x;             // elements between rows of x (BF16: 2 bytes each, E4M3: 1)
   Weight4 w, gate;          // gate.codes null: no gate
   bool mx;                  // MXFP4 weights, else NVFP4

@@ -235,8 +235,8 @@ struct Stager {
   __device__ __forceinline__ uint4* raw(int pair) const { return xs + pair * 32 + (threadIdx.x & 31); }
   __device__ __forceinline__ int k_of(int u) const { return (u0 + u) * kUnit + (threadIdx.x & 31) * 8; }
   __device__ __forceinline__ int scale_of(int m, int k) const {
-    const int b = k >> 5;
-    return p.a.x_swizzled ? (b >> 2) * 512 + m * 16 + (b & 3) : m * static_cast<int>(p.a.K >> 5) + b;
+    const int b = k >> 5, row = p.a.x_row0 + m;
+    return p.a.x_swizzled ? (b >> 2) * 512 + row * 16 + (b & 3) : row * static_cast<int>(p.a.K >> 5) + b;
   }
 
   __device__ __forceinline__ void fetch() const {
@@ -251,7 +251,7 @@ struct Stager {
       } else {
         copy8(dst, static_cast<const uint8_t*>(a.x) + m * a.ld_x + k);
         const int at = scale_of(m, k), word = at & ~3;
-        if (a.x_swizzled || word + 4 <= a.M * static_cast<int>(a.K >> 5))
+        if (a.x_swizzled || word + 4 <= a.x_rows * static_cast<int>(a.K >> 5))
           copy4(dst + 8, a.x_scales + word);
         else  // the last bytes of a linear buffer that ends inside a word
           st_shared4(dst + 8, static_cast<uint32_t>(__ldg(a.x_scales + at)) * 0x01010101u);
@@ -728,7 +728,9 @@ cudaError_t launch_one(const Params& p, int grid, int threads, size_t smem, cuda
 }
 
 // The kernel's shapes.  kNarrow: K no multiple of 64.  kPaired: more than 8 tokens, whose x
-// costs shared memory twice the reads: two 16-row groups share them.
+// costs shared memory twice the reads: two 16-row groups share them (16 tokens: 5376 x 21504
+// 26.3 us against 26.9 with kWide's tiles, 21504 x 5376 22.9 / 23.3, 1024 x 4096 5.0 / 4.7;
+// 8 tokens, 14336 x 4096: 12.8 / 12.1).
 enum Shape { kWide, kNarrow, kPaired };
 
 template <bool MX>
@@ -816,8 +818,7 @@ cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t strea
     second.M = a.M - first.M;
     const int64_t bytes = a.x_scales ? 1 : 2;
     second.x = static_cast<const uint8_t*>(a.x) + first.M * a.ld_x * bytes;
-    // (an MXFP8 scale row: 16 bytes further in the 128 x 4 tiles, K / 32 bytes in rows)
-    if (a.x_scales) second.x_scales = a.x_scales + first.M * (a.x_swizzled ? 16 : a.K / 32);
+    second.x_row0 += first.M;
     second.out = a.out + first.M * a.ld_out;
     const cudaError_t e = launch_matvec(first, launches, stream);
     return e != cudaSuccess ? e : launch_matvec(second, launches, stream);
