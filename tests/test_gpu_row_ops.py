@@ -49,13 +49,30 @@ def test_norm(cuda_device, rows, cols, fmt):
         check(q, v, fmt, layout, ref.NORM_DELTA, where=f"{fmt} {rows}x{cols}")
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 1), (2, 7), (5, 33), (777, 2201), (1, 130001), (3, 65552), (4, 2200)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (2, 7), (5, 33), (9, 3), (19, 8), (17, 1001), (777, 2201), (1, 130001),
+                                       (3, 65552), (4, 2200), (20, 4099), (9, 16365), (9, 16369), (8, 12346)])
 def test_norm_bf16_of_any_size(cuda_device, rows, cols):
     x, r, w = bf16((rows, cols), 1), bf16((rows, cols), 2), bf16((1, cols), 3).view(-1)
-    out, h = nv.rms_norm(x, w, r)
-    v, h64 = ref.norm64(x, r, w, 1e-6)
-    assert np.array_equal(h.double().cpu().numpy(), h64)
-    ref.check_bf16(out, v, ref.NORM_DELTA)
+    for residual, weight in ((r, w), (None, w), (r, None)):
+        res = nv.rms_norm(x, weight, residual, weight_offset=0.5)
+        out, h = res if residual is not None else (res, x)
+        v, h64 = ref.norm64(x, residual, weight, 1e-6, 0.5)
+        assert np.array_equal(h.double().cpu().numpy(), h64)
+        ref.check_bf16(out, v, ref.NORM_DELTA)
+    want, h = nv.rms_norm(x, w, r)
+    # from addresses and strides that take the path of single values
+    wide = torch.zeros((rows + 2, cols + 3), dtype=torch.bfloat16, device="cuda")
+    wide[1:-1, 1:-2] = x
+    assert torch.equal(nv.rms_norm(wide[1:-1, 1:-2], w, r)[1], h)
+    # nothing beside the outputs is written
+    for shift in (16, 15):                               # at a 32-byte address, and at one of single values
+        flat = [torch.full((rows * cols + 32,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        y, ho = (f[shift:shift + rows * cols].view(rows, cols) for f in flat)
+        nv.rms_norm(x, w, r, out=y, residual_out=ho)
+        ref.check_bf16(y, ref.norm64(x, r, w, 1e-6)[0], ref.NORM_DELTA)
+        assert torch.equal(ho, h) and (shift != 16 or torch.equal(y, want))  # (the other path adds in another order)
+        for f in flat:
+            assert (f[:shift] == 7.0).all() and (f[shift + rows * cols:] == 7.0).all()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -190,10 +207,20 @@ def test_nvfp4_sixteen_wide_tail_and_given_scale(cuda_device, op, rows, cols):
     ref.check_blocks(q, ref.norm64(x, None, None, 1e-6)[0] if op == "norm" else v, "nvfp4", "swizzled", delta)
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (100, 333), (64, 1000)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (1, 15), (1, 16), (1, 5001), (100, 333), (64, 1000), (3, 1025)])
 def test_gate_bf16_of_any_size(cuda_device, rows, cols):
     g, u = bf16((rows, cols), 1, 3.0), bf16((rows, cols), 2)
-    ref.check_bf16(nv.silu_mul(g, u), ref.gate64(g, u), ref.GATE_DELTA)
+    want = ref.gate64(g, u)
+    ref.check_bf16(nv.silu_mul(g, u), want, ref.GATE_DELTA)
+    wide = torch.zeros((rows, cols + 3), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:-2] = g
+    ref.check_bf16(nv.silu_mul(wide[:, 1:-2], u), want, ref.GATE_DELTA)
+    flat = torch.full((rows * cols + 32,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = flat[16:16 + rows * cols].view(rows, cols)
+    ref.check_bf16(nv.silu_mul(g, u, out=y), want, ref.GATE_DELTA)
+    assert (flat[:16] == 7.0).all() and (flat[-16:] == 7.0).all()
+    if rows * cols >= 16:
+        ref.check_bf16(nv.silu_mul(g, u, out=g), want, ref.GATE_DELTA)      # in place
 
 
 @pytest.mark.parametrize("cols", [512, 100])

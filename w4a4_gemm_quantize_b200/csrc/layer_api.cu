@@ -207,7 +207,7 @@ nvfp4_status nvfp4_silu_mul(const void* gate, int64_t ld_gate, const void* up, i
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0) return publish_empty(c, s);
   const nvfp4::GateArgs a{static_cast<const uint16_t*>(gate), static_cast<const uint16_t*>(up), ld_gate, ld_up, rows,
-                          cols, false};
+                          cols, false, 0};
   return nvfp4::launch_silu_mul(a, row_output(c), &nvfp4::g_last_launches, s) == cudaSuccess ? NVFP4_OK
                                                                                             : NVFP4_ERR_CUDA;
 }

@@ -41,6 +41,7 @@ struct GateArgs {
   int64_t ld_gate, ld_up;
   int64_t rows, cols;
   bool wide;  // (launcher) rows of both at multiples of 32 bytes
+  int tail;   // (launcher) values behind the last unit of row 0
 };
 
 // Each adds the number of kernels it enqueued to *launches.  rows, cols >= 1.

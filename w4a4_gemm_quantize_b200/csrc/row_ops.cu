@@ -31,6 +31,7 @@ constexpr int kCluster = 8;     // CTAs that share one amax through distributed 
 // Values of a gate that one cluster handles, amax and all, instead of a memset and two
 // launches (8.2 us): 4.1 us for 14336 or 28672, 8.4 us for 114688.
 constexpr int64_t kClusterMax = 128 * 1024;
+constexpr int64_t kMaxFlat = int64_t{1} << 34;  // values of a gate handled as one row (its units fit an int)
 // Threads per row and units per thread of norm_kernel: U = 1 up to 1024 threads, U = 2,
 // 4, 8 up to 512 (64 or 128 registers each); the longest row is 8 x 512 units.
 constexpr int norm_threads(int U) { return U == 1 ? 1024 : 512; }
@@ -456,6 +457,111 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_
   }
 }
 
+// BF16 rows of any width in dense matrices: row r begins s = r cols mod 8 values behind a
+// 16-byte boundary, the same in every matrix, so that the row is read and written in the
+// 16-byte vectors that cover it; the two at its ends go value by value.  The weight, which
+// does not share that shift, is read in words and shifted by half a word for odd s.
+// (8192 x 5375 with a residual: value by value 162 us.)
+template <int V>
+__global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint16_t* out) {
+  __shared__ float sums[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int cols = static_cast<int>(a.cols), T = blockDim.x;
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * cols;
+  const int s = static_cast<int>(start & 7);
+  const int64_t base = start - s;
+  const int nvec = (s + cols + 7) >> 3;
+  const bool add = a.residual != nullptr;
+  auto whole = [&](int j) { return 8 * j >= s && 8 * j - s + 8 <= cols; };
+  // the vector's values inside the row; others are 0
+  auto load = [&](const uint16_t* p, int j, uint32_t (&w)[4]) {
+    if (whole(j)) {
+      const uint4 v = ld_v4(p + base + 8 * j);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 8 * j - s + 2 * i;
+        const uint32_t lo = c >= 0 && c < cols ? p[start + c] : 0u, hi = c + 1 >= 0 && c + 1 < cols ? p[start + c + 1] : 0u;
+        w[i] = lo | (hi << 16);
+      }
+    }
+  };
+  auto store = [&](uint16_t* p, int j, const uint32_t (&w)[4]) {
+    if (whole(j)) {
+      *reinterpret_cast<uint4*>(p + base + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = 8 * j - s + i;
+        if (c >= 0 && c < cols) p[start + c] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+      }
+    }
+  };
+  uint32_t h[V][4], q[V][4];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int j = threadIdx.x + k * T;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[k][i] = q[k][i] = 0u;
+    if (j < nvec) {
+      load(a.x, j, h[k]);
+      if (add) load(a.residual, j, q[k]);
+    }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int j = threadIdx.x + k * T;
+    if (add && j < nvec) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[k][i] = pack_bf16(bf16_lo(h[k][i]) + bf16_lo(q[k][i]), bf16_hi(h[k][i]) + bf16_hi(q[k][i]));
+      store(a.residual_out, j, h[k]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = bf16_lo(h[k][i]), hi = bf16_hi(h[k][i]);
+      sum = __fmaf_rn(hi, hi, __fmaf_rn(lo, lo, sum));
+    }
+  }
+  const float rstd = inv_rms(block_sum(sum, sums), a.cols, a.eps);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int j = threadIdx.x + k * T;
+    if (j >= nvec) break;
+    uint32_t w[5] = {};
+    const int c0 = 8 * j - s;  // column of the vector's first value
+    if (a.weight != nullptr) {
+      // five words from column c0 - (c0 & 1) on, those that hold a column of the row; the
+      // last word of an odd row would reach past it
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(a.weight);
+      const int w0 = c0 >> 1;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const int at = w0 + i;
+        if (at >= 0 && 2 * at + 1 < cols)
+          w[i] = __ldg(words + at);
+        else if (at >= 0 && 2 * at < cols)
+          w[i] = __ldg(a.weight + 2 * at);
+      }
+    }
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo = __fmul_rn(bf16_lo(h[k][i]), rstd), hi = __fmul_rn(bf16_hi(h[k][i]), rstd);
+      if (a.weight != nullptr) {
+        const uint32_t ww = c0 & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+        lo = __fmul_rn(lo, __fadd_rn(bf16_lo(ww), a.weight_offset));
+        hi = __fmul_rn(hi, __fadd_rn(bf16_hi(ww), a.weight_offset));
+      }
+      y[i] = pack_bf16(lo, hi);
+    }
+    store(out, j, y);
+  }
+}
+
 // g / (1 + e^-g) * u of one value, by IEEE operations: the tails, infinities and NaN.
 __device__ __forceinline__ float silu_times(float g, float u) {
   return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
@@ -588,22 +694,38 @@ __global__ void __launch_bounds__(kGateThreads, gate_ctas(FMT, PHASE)) gate_kern
   each(PHASE == kFormat, [&](int r, int u, bool active, const float(&v)[16]) {
     emit<FMT>(v, r, u, active, a.cols, sg, o);
   });
+  if (FMT == NVFP4_OUT_BF16 && blockIdx.x == 0 && static_cast<int>(threadIdx.x) < a.tail) {
+    const int64_t c = a.cols + threadIdx.x;
+    static_cast<uint16_t*>(o.out)[c] = static_cast<uint16_t>(
+        pack_bf16(silu_times(bf16_bits_to_float(a.gate[c]), bf16_bits_to_float(a.up[c])), 0.0f));
+  }
   if (FMT != NVFP4_OUT_BF16 && o.swizzled)
     zero_row_padding(o.scales, a.rows, a.cols / (FMT == NVFP4_OUT_NVFP4 ? 16 : 32),
                      static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
                      static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
-// BF16 values that the 16-value units do not fit.
+// BF16 values that the 16-value units do not fit: 1024 of a row per CTA and step.
 __global__ void __launch_bounds__(256) gate_any_kernel(const GateArgs a, uint16_t* out, int64_t ld_out) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t n = a.rows * a.cols, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
-    const int64_t r = i / a.cols, c = i - r * a.cols;
-    const float v = silu_times(bf16_bits_to_float(a.gate[r * a.ld_gate + c]),
-                               bf16_bits_to_float(a.up[r * a.ld_up + c]));
-    out[r * ld_out + c] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+  const int64_t parts = (a.cols + 1023) / 1024, tasks = a.rows * parts;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int64_t r = task / parts, c0 = (task - r * parts) * 1024 + threadIdx.x;
+    const uint16_t *g = a.gate + r * a.ld_gate, *u = a.up + r * a.ld_up;
+    uint16_t* y = out + r * ld_out;
+    float gv[4], uv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t c = c0 + 256 * i;
+      gv[i] = c < a.cols ? bf16_bits_to_float(g[c]) : 0.0f;
+      uv[i] = c < a.cols ? bf16_bits_to_float(u[c]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t c = c0 + 256 * i;
+      if (c < a.cols) y[c] = static_cast<uint16_t>(pack_bf16(silu_times(gv[i], uv[i]), 0.0f));
+    }
   }
 }
 
@@ -638,6 +760,13 @@ cudaError_t launch(void (*kernel)(KArgs...), int64_t grid, int threads, int clus
 
 bool fits_units(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
 bool fits_wide(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld % 16 == 0; }
+
+// Whether every matrix of a BF16 norm lies dense from a 16-byte boundary on.
+bool dense(const NormArgs& a, const RowOutput& o) {
+  auto one = [&](const void* p, int64_t ld) { return fits_units(p, 0) && (ld == a.cols || a.rows == 1); };
+  return one(a.x, a.ld_x) && one(o.out, o.ld_out) && (reinterpret_cast<uintptr_t>(a.weight) & 3u) == 0 &&
+         (!a.residual || (one(a.residual, a.ld_res) && one(a.residual_out, a.ld_res_out)));
+}
 
 template <int FMT, int PHASE>
 cudaError_t norm_launch_u(const NormArgs& a, const RowOutput& o, int* launches, cudaStream_t stream) {
@@ -688,6 +817,15 @@ cudaError_t launch_rms_norm(const NormArgs& args, const RowOutput& output, int* 
   switch (o.format) {
     case NVFP4_OUT_BF16:
       if (units && fits_units(o.out, o.ld_out)) return norm_launch_u<NVFP4_OUT_BF16, kOnePass>(a, o, launches, stream);
+      if (dense(a, o) && a.cols <= 8 * 512 * 4 - 16) {
+        const int64_t nvec = (a.cols + 14) / 8;  // at most, whatever the shift
+        const int V = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+        const int T = static_cast<int>(((nvec + V - 1) / V + 31) / 32 * 32);
+        uint16_t* y = static_cast<uint16_t*>(o.out);
+        return V == 1   ? launch(norm_dense_kernel<1>, a.rows, T, 1, stream, launches, a, y)
+               : V == 2 ? launch(norm_dense_kernel<2>, a.rows, T, 1, stream, launches, a, y)
+                        : launch(norm_dense_kernel<4>, a.rows, T, 1, stream, launches, a, y);
+      }
       if (a.cols <= 512 * kAny) {
         const int T = static_cast<int>(((a.cols + kAny - 1) / kAny + 31) / 32 * 32);
         return launch(norm_any_kernel<true>, a.rows, T, 1, stream, launches, a, static_cast<uint16_t*>(o.out), o.ld_out);
@@ -713,10 +851,21 @@ cudaError_t launch_silu_mul(const GateArgs& args, const RowOutput& output, int* 
   o.wide = fits_wide(o.out, o.ld_out);
   switch (o.format) {
     case NVFP4_OUT_BF16: {
+      const int64_t n = a.rows * a.cols;
+      if (a.cols % kUnit != 0 && n >= kUnit && n <= kMaxFlat &&
+          (a.rows == 1 || (a.ld_gate == a.cols && a.ld_up == a.cols && o.ld_out == a.cols)) && fits_units(a.gate, 0) && fits_units(a.up, 0) && fits_units(o.out, 0)) {
+        // dense matrices of any width: one row of all values, whose last few are a tail
+        a.rows = 1;
+        a.tail = static_cast<int>(n % kUnit);
+        a.cols = a.ld_gate = a.ld_up = o.ld_out = n - a.tail;
+        a.wide = fits_wide(a.gate, 0) && fits_wide(a.up, 0);
+        o.wide = fits_wide(o.out, 0);
+        return gate_launch<NVFP4_OUT_BF16, kOnePass>(a, o, launches, stream);
+      }
       if (a.cols % kUnit == 0 && fits_units(a.gate, a.ld_gate) && fits_units(a.up, a.ld_up) &&
           fits_units(o.out, o.ld_out))
         return gate_launch<NVFP4_OUT_BF16, kOnePass>(a, o, launches, stream);
-      int64_t grid = (a.rows * a.cols + 255) / 256;
+      int64_t grid = a.rows * ((a.cols + 1023) / 1024);
       const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
       if (grid > cap) grid = cap;
       return launch(gate_any_kernel, grid, 256, 1, stream, launches, a, static_cast<uint16_t*>(o.out), o.ld_out);
