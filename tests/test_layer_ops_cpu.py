@@ -169,3 +169,20 @@ def test_reference_roundings_agree_with_torch_and_the_oracle_grid():
     y = np.linspace(0, 8, 10007)
     near = np.min(np.abs(y[:, None] - ref.E2M1[None]), axis=1)
     assert np.allclose(np.abs(ref.round_e2m1(y) - y), near)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_matvec_refuses_an_output_over_swizzled_activation_scales(lib, mx):
+    """Swizzled scales take whole 128 x 4 tiles: 4 x 256 values' scales lie in 1024 bytes, not in the 32 they are."""
+    S, W = 6 << 20, 2 << 20
+
+    def mv(out, layout):
+        tail = [] if mx else [P(0)]
+        gs = [] if mx else [P(4 << 20)]
+        call = lib.mxfp4_matvec if mx else lib.nvfp4_matvec
+        return call(P(1 << 20), P(S), layout, 4, 256, 256, P(W), P(3 << 20), *gs, P(0), P(0), *tail, 96, P(out), 96, None)
+
+    for out in (S, S + 32, S + 560, S + 1022, S - 700):
+        assert mv(out, 0) == 1, out
+    assert mv(S + 1024, 0) in NO_DEVICE and mv(S - 768, 0) in NO_DEVICE   # the output has 4 x 96 x 2 = 768 bytes
+    assert mv(S + 30, 1) == 1 and mv(S + 32, 1) in NO_DEVICE              # linear: 32 bytes

@@ -121,7 +121,9 @@ nvfp4_status matvec(const void* x, const uint8_t* x_scales, int x_layout, int64_
     return NVFP4_ERR_ALIGNMENT;
   const Region o{out, M, N, ld_out, 2};
   const int64_t codes = N * (K / 2), scales = (N + 127) / 128 * 128 * ((K / (mx ? 32 : 16) + 3) / 4 * 4);
-  if (overlap(o, {x, M, K, ld_x, x_scales ? 1 : 2}) || overlap(o, {x_scales, 1, M * (K / 32), M * (K / 32), 1}))
+  const int64_t xs =  // swizzled: whole 128 x 4 tiles
+      x_scales ? static_cast<int64_t>(mxfp4_scales_bytes(M, K, static_cast<nvfp4_sf_layout>(x_layout))) : 0;
+  if (overlap(o, {x, M, K, ld_x, x_scales ? 1 : 2}) || overlap(o, {x_scales, 1, xs, xs, 1}))
     return NVFP4_ERR_INVALID_ARG;
   for (const nvfp4::Weight4& t : {w, gate})
     if (overlap(o, {t.codes, 1, codes, codes, 1}) || overlap(o, {t.scales, 1, scales, scales, 1}))
