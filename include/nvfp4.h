@@ -321,7 +321,8 @@ size_t nvfp4_row_workspace_bytes(void);
  *   global_scale_out NVFP4: device float or NULL, receives the tensor scale.
  *   workspace    nvfp4_row_workspace_bytes() bytes; read only for NVFP4 without a given scale.
  *   rows >= 0, rows <= 2^30; cols >= 1; the block formats: cols <= 65536 (SHAPE).
- * Outputs must not overlap the inputs or one another except as stated (INVALID_ARG).
+ * Outputs and the workspace must not overlap the inputs or one another except as stated
+ * (INVALID_ARG); global_scale_out may be global_scale_in.
  * Errors: INVALID_ARG, SHAPE, ALIGNMENT, WORKSPACE, UNSUPPORTED_DEVICE, CUDA. */
 nvfp4_status nvfp4_rms_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, const void *residual,
                             int64_t ld_residual, void *residual_out, int64_t ld_residual_out, const void *weight,

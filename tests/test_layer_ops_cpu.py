@@ -186,3 +186,26 @@ def test_matvec_refuses_an_output_over_swizzled_activation_scales(lib, mx):
         assert mv(out, 0) == 1, out
     assert mv(S + 1024, 0) in NO_DEVICE and mv(S - 768, 0) in NO_DEVICE   # the output has 4 x 96 x 2 = 768 bytes
     assert mv(S + 30, 1) == 1 and mv(S + 32, 1) in NO_DEVICE              # linear: 32 bytes
+
+
+def test_tensor_scales_and_workspace_share_no_byte_with_other_arguments(lib):
+    """The 4-byte tensor scales are inputs and outputs like the matrices, and the workspace is written."""
+    X, OUT, SC, GI, GO, WS = (i << 20 for i in range(1, 7))
+    for call in (lambda **k: norm(lib, x=X, out=OUT, fmt=3, scales=SC, ws_bytes=256, **k),
+                 lambda **k: gate(lib, g=X, u=9 << 20, out=OUT, fmt=3, scales=SC, ws_bytes=256, **k)):
+        assert call(gs=GI, gs_out=GO) in NO_DEVICE and call(ws=WS, gs_out=GO) in NO_DEVICE
+        assert call(gs=GI, gs_out=GI) in NO_DEVICE                     # the given scale, in place
+        for taken in (X, OUT, SC):
+            assert call(gs=GI, gs_out=taken + 8) == 1
+            assert call(ws=taken + 16, gs_out=GO) == 1
+        for output in (OUT, SC):
+            assert call(gs=output + 8, gs_out=GO) == 1
+        assert call(ws=WS, gs_out=WS + 252) == 1 and call(ws=WS, gs_out=WS + 256) in NO_DEVICE
+    assert norm(lib, x=X, res=7 << 20, res_out=8 << 20, out=OUT, fmt=3, scales=SC, gs=(8 << 20) + 4, gs_out=GO) == 1
+    assert norm(lib, x=X, weight=10 << 20, out=OUT, fmt=3, scales=SC, gs=GI, gs_out=10 << 20) == 1
+
+    def mv(gs, ggs, out):
+        return lib.nvfp4_matvec(P(X), P(0), 0, 4, 64, 64, P(OUT), P(SC), P(gs), P(7 << 20), P(8 << 20), P(ggs), 96,
+                                P(out), 96, None)
+    assert mv(GI, GO, WS) in NO_DEVICE
+    assert mv(WS + 4, GO, WS) == 1 and mv(GI, WS + 4, WS) == 1

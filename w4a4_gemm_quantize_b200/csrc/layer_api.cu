@@ -64,6 +64,24 @@ Region out_region(const RowCall& c) {
   return {c.out, 1, bytes, bytes, 1};
 }
 
+// Whether `bytes` bytes at p lie in a region (not in the gaps between its rows).
+bool inside(const void* p, int64_t bytes, const Region& r) {
+  return overlap(r, {p, p ? 1 : 0, bytes / r.size, r.ld, r.size});
+}
+
+// Whether a tensor scale or the workspace shares a byte with another argument: none may, but
+// for the given scale written over itself.  rin: inputs, rout: outputs.
+template <size_t I, size_t O>
+bool words_overlap(const RowCall& c, const Region (&rin)[I], const Region (&rout)[O]) {
+  const void* ws = c.format == NVFP4_OUT_NVFP4 && !c.gs_in ? c.workspace : nullptr;
+  constexpr int64_t kWs = kRowWorkspace;
+  for (const Region& r : rin)
+    if (inside(c.gs_out, 4, r) || inside(ws, kWs, r)) return true;
+  for (const Region& r : rout)
+    if (inside(c.gs_in, 4, r) || inside(c.gs_out, 4, r) || inside(ws, kWs, r)) return true;
+  return inside(c.gs_out, 4, {ws, ws ? 1 : 0, kWs, kWs, 1});
+}
+
 // The checks of the output's side that need no look at the inputs.
 nvfp4_status validate_output(const RowCall& c) {
   if (c.rows < 0 || c.cols < 1) return NVFP4_ERR_INVALID_ARG;
@@ -126,7 +144,8 @@ nvfp4_status matvec(const void* x, const uint8_t* x_scales, int x_layout, int64_
   if (overlap(o, {x, M, K, ld_x, x_scales ? 1 : 2}) || overlap(o, {x_scales, 1, xs, xs, 1}))
     return NVFP4_ERR_INVALID_ARG;
   for (const nvfp4::Weight4& t : {w, gate})
-    if (overlap(o, {t.codes, 1, codes, codes, 1}) || overlap(o, {t.scales, 1, scales, scales, 1}))
+    if (overlap(o, {t.codes, 1, codes, codes, 1}) || overlap(o, {t.scales, 1, scales, scales, 1}) ||
+        inside(t.gs, 4, o))
       return NVFP4_ERR_INVALID_ARG;
   const nvfp4_status st = nvfp4_check_device();
   if (st != NVFP4_OK || M == 0) return st;
@@ -175,6 +194,7 @@ nvfp4_status nvfp4_rms_norm(const void* x, int64_t rows, int64_t cols, int64_t l
     if (overlap(y, in) && (block || !same_place(y, in))) return NVFP4_ERR_INVALID_ARG;
   for (const Region& other : {rx, rr, ro, rw, y})
     if (overlap(sc, other)) return NVFP4_ERR_INVALID_ARG;
+  if (words_overlap(c, {rx, rr, rw}, {y, ro, sc})) return NVFP4_ERR_INVALID_ARG;
   st = nvfp4_check_device();
   if (st != NVFP4_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -204,6 +224,7 @@ nvfp4_status nvfp4_silu_mul(const void* gate, int64_t ld_gate, const void* up, i
     if (overlap(y, in) && (block || !same_place(y, in))) return NVFP4_ERR_INVALID_ARG;
   for (const Region& other : {rg, ru, y})
     if (overlap(sc, other)) return NVFP4_ERR_INVALID_ARG;
+  if (words_overlap(c, {rg, ru}, {y, sc})) return NVFP4_ERR_INVALID_ARG;
   st = nvfp4_check_device();
   if (st != NVFP4_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
