@@ -304,8 +304,9 @@ size_t nvfp4_row_workspace_bytes(void);
  *   h = BF16(x + residual)  (h = x without a residual), stored to residual_out;
  *   v = (h r) (weight + weight_offset),  r = 1 / sqrt(mean over the row of h^2 + eps),
  * sums and v in FP32.  The norm sees the rounded h, the value that the residual stream
- * keeps, so the call equals an addition in BF16 followed by a norm.  (A row whose mean
- * square overflows FP32 becomes 0; one with a NaN or an infinity follows the formula.)
+ * keeps, so the call equals an addition in BF16 followed by a norm.  Rows of any finite
+ * magnitude are normalised, also where their squares leave FP32's range; one with a NaN or
+ * an infinity, or of zeros under eps 0, follows the formula.
  *   x            device, BF16, rows x cols, row stride ld_x.
  *   residual     device, BF16, rows x cols, row stride ld_residual, or NULL.
  *   residual_out device, BF16, rows x cols, row stride ld_residual_out; NULL exactly when

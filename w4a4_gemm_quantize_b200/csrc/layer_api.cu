@@ -201,7 +201,7 @@ nvfp4_status nvfp4_rms_norm(const void* x, int64_t rows, int64_t cols, int64_t l
   if (rows == 0) return publish_empty(c, s);
   const nvfp4::NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual),
                           static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(residual_out), ld_x,
-                          ld_residual, ld_residual_out, rows, cols, eps, weight_offset, false};
+                          ld_residual, ld_residual_out, rows, cols, eps, weight_offset, 0.0f, 0.0f, false};
   return nvfp4::launch_rms_norm(a, row_output(c), &nvfp4::g_last_launches, s) == cudaSuccess ? NVFP4_OK
                                                                                             : NVFP4_ERR_CUDA;
 }

@@ -32,6 +32,7 @@ struct NormArgs {
   int64_t ld_x, ld_res, ld_res_out;
   int64_t rows, cols;
   float eps, weight_offset;
+  float inv_cols, inv_cols_lo;  // (launcher) 1 / cols, in two floats
   bool wide;  // (launcher) rows of every matrix but the output at multiples of 32 bytes
 };
 

@@ -139,6 +139,14 @@ __device__ __forceinline__ float exp2_int(int k) {  // k in [-127, 127]
   return k >= -126 ? __uint_as_float(static_cast<uint32_t>(k + 127) << 23) : __uint_as_float(0x00400000u);
 }
 
+// The words again, for the compiler unknown ones: it keeps them, not the floats they were widened
+// to before (twice the registers; 8192 x 5375: 84 us instead of 72).
+template <int N>
+__device__ __forceinline__ void as_words(uint32_t (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(w[i]));
+}
+
 // Writes unit u (values 16 u .. 16 u + 15) of row r.  Every lane of the warp calls it
 // with u = a multiple of 32 + lane; `active`: u is inside the row.
 template <int FMT>
@@ -251,13 +259,14 @@ __device__ __forceinline__ float cluster_max(float mine, float* slot) {
 
 // Sum over the CTA (every thread gets it), in a fixed order.  One __syncthreads; `part`
 // must not be reused before another one.
-__device__ __forceinline__ float block_sum(float s, float* part) {
+template <typename T>
+__device__ __forceinline__ T block_sum(T s, T* part) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
   const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   if (lane == 0) part[threadIdx.x >> 5] = s;
   __syncthreads();
-  s = lane < nw ? part[lane] : 0.0f;
+  s = lane < nw ? part[lane] : T{0};
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
   return s;
@@ -273,15 +282,75 @@ __device__ __forceinline__ float block_max(float m, uint32_t* part) {
   return __uint_as_float(b);
 }
 
-__device__ __forceinline__ float inv_rms(float sum_sq, int64_t cols, float eps) {
-  return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum_sq, static_cast<float>(cols)), eps));
+// 1 / sqrt(mean square + eps) = up * r, up a power of two and r in (1/2, 1] (above that where up
+// would leave binary32).  h * up is exact and near 1, whatever the row's magnitude.
+struct InvRms {
+  float up, r;
+};
+
+__device__ __forceinline__ float exp2_float(int k) {  // k in [-149, 127]
+  return __int_as_float(k >= -126 ? (k + 127) << 23 : 1 << (k + 149));
+}
+
+// From m = (mean square + eps) 4^f.  With m = 4^k t, t in [1, 4): r = 1 / sqrt(t) by the function
+// and one Newton step, r + r (1 - t r^2) / 2, whose residual takes r^2 in two floats.
+__device__ __forceinline__ InvRms inv_rms(float m, int f) {
+  if (!(m >= 0x1p-126f && m < __int_as_float(0x7F800000)))  // zero, infinity, NaN
+    return {1.0f, m > 0.0f ? 0.0f : m == 0.0f ? __int_as_float(0x7F800000) : m};
+  const int e = (__float_as_int(m) >> 23) - 127, k = e >> 1;
+  const float t = __int_as_float(__float_as_int(m) - (k << 24));
+  const float r = rsqrtf(t), q = __fmul_rn(r, r);
+  const float d = __fmaf_rn(-t, __fmaf_rn(r, r, -q), __fmaf_rn(-t, q, 1.0f));
+  const int up = max(-149, min(127, f - k));
+  return {exp2_float(up), __fmul_rn(__fmaf_rn(0.5f * r, d, r), exp2_float(f - k - up))};
+}
+
+// Sum over the CTA of (h x)^2, h the row's values from memory.  Out of line, for the few rows that
+// need it: inlined, the branch cost 8192 x 5375 86 us instead of 75.
+__device__ __noinline__ float scaled_squares(const uint16_t* h, int64_t cols, float x, float* part) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) {
+    const float v = bf16_bits_to_float(h[c]) * x;
+    s = __fmaf_rn(v, v, s);
+  }
+  return block_sum(s, part);
+}
+
+// The same of a row, from this thread's part of the sum of squares.  BF16 squares reach from
+// 2^-266 to 2^256: a sum that left binary32's range, or came near its lower end with nothing in
+// eps to cover that, is taken once more of scaled values.  h: the row's cols values in memory (0:
+// no row), the CTA's own stores of them visible since the first sum's barrier.
+__device__ __forceinline__ InvRms row_inv_rms(const NormArgs& a, float mine, float (*part)[32], const uint16_t* h,
+                                              int64_t cols) {
+  const float s = block_sum(mine, part[0]);
+  const float m = __fmaf_rn(s, a.inv_cols, __fmaf_rn(s, a.inv_cols_lo, a.eps));
+  if (s < 1e38f && m >= 0x1p-100f) return inv_rms(m, 0);
+  const int f = s < 1e38f ? 80 : -80;
+  const float x = scaled_squares(h, cols, exp2_float(f), part[1]), eps = a.eps * exp2_float(f) * exp2_float(f);
+  return inv_rms(__fmaf_rn(x, a.inv_cols, eps), f);
+}
+
+// Sum of squares of the values of N words of BF16 pairs, in four parts.
+template <int N>
+__device__ __forceinline__ float unit_squares(const uint32_t (&h)[N]) {
+  uint64_t s[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t x = pack2(bf16_lo(h[i]), bf16_hi(h[i]));
+    s[i & 1] = fma2(x, x, s[i & 1]);
+  }
+  float a, b, c, d;
+  unpack2(s[0], a, b);
+  unpack2(s[1], c, d);
+  return (a + b) + (c + d);
 }
 
 // One CTA per row; thread t owns units t, t + T, ... (U of them), kept in registers
 // between the sum of squares and the output, so each input is read once.
 template <int FMT, int U, int PHASE>
 __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a, const RowOutput o) {
-  __shared__ float sums[32];
+  __shared__ float sums[2][32];
   __shared__ uint32_t maxima[32];
   __shared__ float cta_max;
   grid_dependency_wait();
@@ -298,7 +367,6 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
   const int64_t r = PHASE == kFormat ? a.rows - 1 - blockIdx.x : blockIdx.x;
   const bool row = PHASE != kCluster1 || r < a.rows;
   uint32_t h[U][8];
-  float s = 0.0f;
   const bool add = PHASE != kFormat && a.residual != nullptr;
   const uint16_t* src = PHASE == kFormat && a.residual ? a.residual_out + r * a.ld_res_out : a.x + r * a.ld_x;
 #pragma unroll
@@ -342,20 +410,20 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
       }
     }
   }
+  float s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    float v[16];
-    widen(h[k], v);
+  for (int k = 0; k < U; ++k) s += unit_squares(h[k]);
+  const InvRms inv = row_inv_rms(a, s, sums, add ? a.residual_out + r * a.ld_res_out : src, row ? a.cols : 0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s = __fmaf_rn(v[i], v[i], s);
-  }
-  const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
+  for (int k = 0; k < U; ++k) as_words(h[k]);
+  const uint64_t up = pack2(inv.up, inv.up), rstd = pack2(inv.r, inv.r), one = pack2(1.0f, 1.0f);
+  const uint64_t offset = pack2(a.weight_offset, a.weight_offset);
 
   auto values = [&](int k, float (&v)[16]) {
     const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
-    widen(h[k], v);
+    uint64_t x[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], rstd);
+    for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(pack2(bf16_lo(h[k][i]), bf16_hi(h[k][i])), up), rstd);
     if (a.weight != nullptr && u < units) {
       uint32_t w[8];
 #pragma unroll
@@ -364,11 +432,10 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
         w[4 * half] = q.x, w[4 * half + 1] = q.y, w[4 * half + 2] = q.z, w[4 * half + 3] = q.w;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[2 * i] = __fmul_rn(v[2 * i], __fadd_rn(bf16_lo(w[i]), a.weight_offset));
-        v[2 * i + 1] = __fmul_rn(v[2 * i + 1], __fadd_rn(bf16_hi(w[i]), a.weight_offset));
-      }
+      for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], fma2(pack2(bf16_lo(w[i]), bf16_hi(w[i])), one, offset));
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpack2(x[i], v[2 * i], v[2 * i + 1]);
   };
 
   float sg = 1.0f;
@@ -412,7 +479,6 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
 constexpr int kAny = 8;
 template <bool CACHED>
 __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_t* out, int64_t ld_out) {
-  __shared__ float sums[32];
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t r = blockIdx.x;
@@ -426,34 +492,40 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_
     ho[c] = static_cast<uint16_t>(h);
     return bf16_bits_to_float(h);
   };
-  auto finish = [&](int64_t c, float f, float rstd) {
-    float v = __fmul_rn(f, rstd);
+  auto finish = [&](int64_t c, float f, InvRms inv) {
+    float v = __fmul_rn(__fmul_rn(f, inv.up), inv.r);
     if (a.weight) v = __fmul_rn(v, __fadd_rn(bf16_bits_to_float(a.weight[c]), a.weight_offset));
     out[r * ld_out + c] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
   };
-  float s = 0.0f;
   if constexpr (CACHED) {
+    __shared__ float sums[2][32];
     float f[kAny];
 #pragma unroll
     for (int i = 0; i < kAny; ++i) {
       const int64_t c = threadIdx.x + i * static_cast<int64_t>(blockDim.x);
       f[i] = c < a.cols ? value(c) : 0.0f;
-      s = __fmaf_rn(f[i], f[i], s);
     }
-    const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kAny; ++i) s = __fmaf_rn(f[i], f[i], s);
+    const InvRms inv = row_inv_rms(a, s, sums, q ? ho : x, a.cols);
 #pragma unroll
     for (int i = 0; i < kAny; ++i) {
       const int64_t c = threadIdx.x + i * static_cast<int64_t>(blockDim.x);
-      if (c < a.cols) finish(c, f[i], rstd);
+      if (c < a.cols) finish(c, f[i], inv);
     }
   } else {
+    __shared__ double sums[32];
+    double s = 0.0;  // (the row may have 2^31 values, and they are read once: no second sum)
     for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
-      const float f = value(c);
-      s = __fmaf_rn(f, f, s);
+      const double f = value(c);
+      s = __fma_rn(f, f, s);
     }
-    const float rstd = inv_rms(block_sum(s, sums), a.cols, a.eps);
+    const double m = block_sum(s, sums) / static_cast<double>(a.cols) + static_cast<double>(a.eps);
+    const int f = m > 0x1p100 && m < 0x1p300 ? -80 : m < 0x1p-100 ? 80 : 0;
+    const InvRms inv = inv_rms(static_cast<float>(m * (f < 0 ? 0x1p-160 : f > 0 ? 0x1p160 : 1.0)), f);
     const uint16_t* h = q ? ho : x;
-    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) finish(c, bf16_bits_to_float(h[c]), rstd);
+    for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) finish(c, bf16_bits_to_float(h[c]), inv);
   }
 }
 
@@ -464,7 +536,7 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_
 // (8192 x 5375 with a residual: 73 us; value by value 162.)
 template <int V>
 __global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint16_t* out) {
-  __shared__ float sums[32];
+  __shared__ float sums[2][32];
   grid_dependency_wait();
   grid_dependents_launch();
   const int cols = static_cast<int>(a.cols), T = blockDim.x;
@@ -510,7 +582,6 @@ __global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint1
       if (add) load(a.residual, j, q[k]);
     }
   }
-  float sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int j = threadIdx.x + k * T;
@@ -520,13 +591,13 @@ __global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint1
         h[k][i] = pack_bf16(bf16_lo(h[k][i]) + bf16_lo(q[k][i]), bf16_hi(h[k][i]) + bf16_hi(q[k][i]));
       store(a.residual_out, j, h[k]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float lo = bf16_lo(h[k][i]), hi = bf16_hi(h[k][i]);
-      sum = __fmaf_rn(hi, hi, __fmaf_rn(lo, lo, sum));
-    }
   }
-  const float rstd = inv_rms(block_sum(sum, sums), a.cols, a.eps);
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum += unit_squares(h[k]);
+  const InvRms inv = row_inv_rms(a, sum, sums, (add ? a.residual_out : a.x) + start, a.cols);
+#pragma unroll
+  for (int k = 0; k < V; ++k) as_words(h[k]);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int j = threadIdx.x + k * T;
@@ -550,7 +621,8 @@ __global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint1
     uint32_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float lo = __fmul_rn(bf16_lo(h[k][i]), rstd), hi = __fmul_rn(bf16_hi(h[k][i]), rstd);
+      float lo = __fmul_rn(__fmul_rn(bf16_lo(h[k][i]), inv.up), inv.r);
+      float hi = __fmul_rn(__fmul_rn(bf16_hi(h[k][i]), inv.up), inv.r);
       if (a.weight != nullptr) {
         const uint32_t ww = c0 & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
         lo = __fmul_rn(lo, __fadd_rn(bf16_lo(ww), a.weight_offset));
@@ -808,6 +880,9 @@ cudaError_t gate_launch(const GateArgs& a, const RowOutput& o, int* launches, cu
 cudaError_t launch_rms_norm(const NormArgs& args, const RowOutput& output, int* launches, cudaStream_t stream) {
   NormArgs a = args;
   RowOutput o = output;
+  const double inv_cols = 1.0 / static_cast<double>(a.cols);
+  a.inv_cols = static_cast<float>(inv_cols);
+  a.inv_cols_lo = static_cast<float>(inv_cols - a.inv_cols);
   a.wide = fits_wide(a.x, a.ld_x) &&
            (!a.residual || (fits_wide(a.residual, a.ld_res) && fits_wide(a.residual_out, a.ld_res_out)));
   o.wide = fits_wide(o.out, o.ld_out);
