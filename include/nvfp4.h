@@ -302,8 +302,9 @@ size_t nvfp4_row_workspace_bytes(void);
 
 /* Root-mean-square norm of a BF16 matrix, with the residual's addition before it:
  *   h = BF16(x + residual)  (h = x without a residual), stored to residual_out;
- *   v = (h r) (weight + weight_offset),  r = 1 / sqrt(mean over the row of h^2 + eps),
- * sums and v in FP32.  The norm sees the rounded h, the value that the residual stream
+ *   v = h (weight + weight_offset) r,  r = 1 / sqrt(mean over the row of h^2 + eps),
+ * sums and v in FP32 (the product before r: exact for a BF16 factor; NVFP4's computed scale
+ * from v in FP64).  The norm sees the rounded h, the value that the residual stream
  * keeps, so the call equals an addition in BF16 followed by a norm.  Rows of any finite
  * magnitude are normalised, also where their squares leave FP32's range; one with a NaN or
  * an infinity, or of zeros under eps 0, follows the formula.

@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr size_t kRowWorkspace = 256;  // word 0: the output's amax
+constexpr size_t kRowWorkspace = 256;  // the first 8 bytes: the output's amax
 constexpr int64_t kMaxRows = int64_t{1} << 30;
 constexpr int64_t kMaxBlockCols = 65536;
 
@@ -120,7 +120,7 @@ nvfp4_status publish_empty(const RowCall& c, cudaStream_t s) {
 
 nvfp4::RowOutput row_output(const RowCall& c) {
   return {c.out,   c.ld_out, c.scales, c.layout == NVFP4_SF_SWIZZLED, c.format, c.gs_in, c.gs_out,
-          static_cast<uint32_t*>(c.workspace), false};
+          static_cast<unsigned long long*>(c.workspace), false};
 }
 
 nvfp4_status matvec(const void* x, const uint8_t* x_scales, int x_layout, int64_t M, int64_t K, int64_t ld_x,

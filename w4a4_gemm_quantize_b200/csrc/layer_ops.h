@@ -20,7 +20,7 @@ struct RowOutput {
   int format;
   const float* gs_in;  // NVFP4: the given tensor scale, or null: computed from the output's amax
   float* gs_out;       // NVFP4: receives the tensor scale (may be null)
-  uint32_t* amax_word; // NVFP4 without gs_in: one word of scratch
+  unsigned long long* amax_word;  // NVFP4 without gs_in: scratch for the output's amax (binary64)
   bool wide;           // (launchers) BF16 rows of out at multiples of 32 bytes
 };
 

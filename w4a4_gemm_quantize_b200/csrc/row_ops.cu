@@ -1,6 +1,7 @@
 // row_ops.cu -- the operators around a layer's products, with the quantizer fused in:
 //   rms_norm: h = BF16(x + residual) (kept as the new residual stream),
-//             v = (h r)(w + offset), r = 1/sqrt(mean(h^2) + eps);
+//             v = h (w + offset) r, r = 1/sqrt(mean(h^2) + eps), rounded once where w + offset has
+//             16 bits or fewer;
 //   silu_mul: v = g / (1 + e^-g) * u;
 // and v leaves as BF16, MXFP8, MXFP4 or NVFP4.  The block scales and codes are taken
 // from v in binary32, not from a BF16 copy of it, so a block format rounds once.
@@ -124,8 +125,20 @@ __device__ __forceinline__ float amax16(const float (&v)[16]) {
   return max_nan(m, fabsf(v[15]));
 }
 
-// s_g of an output whose largest magnitude is amax
-__device__ __forceinline__ float tensor_scale(float amax) { return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 2688.0f); }
+// s_g of an output whose largest magnitude is amax (a division in binary64 instead of the product,
+// which is off by 2^-52 before the rounding to a float: 8192 x 5376, two launches, 84.0 us, not 82.8)
+__device__ __forceinline__ float tensor_scale(double amax) {
+  return amax == 0.0 ? 1.0f : static_cast<float>(amax * (1.0 / 2688.0));
+}
+
+// amax >= 0 or NaN: the bit patterns order like the values, NaN above all
+__device__ __forceinline__ unsigned long long amax_bits(double amax) {
+  return static_cast<unsigned long long>(__double_as_longlong(amax)) & 0x7FFFFFFFFFFFFFFFull;
+}
+
+__device__ __forceinline__ void publish_amax(double amax, unsigned long long* word) {
+  if (amax_bits(amax) != 0u) atomicMax(word, amax_bits(amax));
+}
 
 // shared exponent of an MX block: floor(log2 amax) - emax, clamped (amax = 0: -127)
 __device__ __forceinline__ int mx_exponent(float amax, int emax) {
@@ -246,15 +259,21 @@ int64_t padding_lines(int64_t rows, int64_t cols, const RowOutput& o) {
   return (nblk + 3) / 4 * 32;
 }
 
-__device__ __forceinline__ float cluster_max(float mine, float* slot) {
-  // mine >= 0 or NaN: the bit patterns order like the values, NaN above all
-  if (threadIdx.x == 0) *slot = mine;
+__device__ __forceinline__ unsigned long long ld_shared_cluster_u64(uint32_t cluster_addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ double cluster_max(double mine, unsigned long long* slot) {
+  if (threadIdx.x == 0) *slot = amax_bits(mine);
   cluster_sync();
-  uint32_t g = 0;
+  unsigned long long g = 0;
+#pragma unroll
   for (uint32_t i = 0; i < static_cast<uint32_t>(kCluster); ++i)
-    g = max(g, ld_shared_cluster_u32(mapa_shared(smem_u32(slot), i)));
+    g = max(g, ld_shared_cluster_u64(mapa_shared(smem_u32(slot), i)));
   cluster_sync();  // no CTA leaves while another still reads its word
-  return __uint_as_float(g);
+  return __longlong_as_double(static_cast<long long>(g));
 }
 
 // Sum over the CTA (every thread gets it), in a fixed order.  One __syncthreads; `part`
@@ -282,27 +301,29 @@ __device__ __forceinline__ float block_max(float m, uint32_t* part) {
   return __uint_as_float(b);
 }
 
-// 1 / sqrt(mean square + eps) = up * r, up a power of two and r in (1/2, 1] (above that where up
-// would leave binary32).  h * up is exact and near 1, whatever the row's magnitude.
+// 1 / sqrt(mean square + eps) = up (r + r_lo), up a power of two and r in [1, 2] (above that where
+// up would leave binary32), r_lo what its float leaves.  h * up is exact and near 1, whatever the
+// row's magnitude; its product with a BF16 weight is exact too, so that v is rounded once, by r.
 struct InvRms {
-  float up, r;
+  float up, r, r_lo;
 };
 
 __device__ __forceinline__ float exp2_float(int k) {  // k in [-149, 127]
   return __int_as_float(k >= -126 ? (k + 127) << 23 : 1 << (k + 149));
 }
 
-// From m = (mean square + eps) 4^f.  With m = 4^k t, t in [1, 4): r = 1 / sqrt(t) by the function
-// and one Newton step, r + r (1 - t r^2) / 2, whose residual takes r^2 in two floats.
+// From m = (mean square + eps) 4^f.  With m = 4^k t, t in [1, 4): r = 2 / sqrt(t) by the function
+// and one Newton step, r + r (1 - t (r / 2)^2) / 2, whose residual takes the square in two floats.
 __device__ __forceinline__ InvRms inv_rms(float m, int f) {
   if (!(m >= 0x1p-126f && m < __int_as_float(0x7F800000)))  // zero, infinity, NaN
-    return {1.0f, m > 0.0f ? 0.0f : m == 0.0f ? __int_as_float(0x7F800000) : m};
+    return {1.0f, m > 0.0f ? 0.0f : m == 0.0f ? __int_as_float(0x7F800000) : m, 0.0f};
   const int e = (__float_as_int(m) >> 23) - 127, k = e >> 1;
   const float t = __int_as_float(__float_as_int(m) - (k << 24));
   const float r = rsqrtf(t), q = __fmul_rn(r, r);
   const float d = __fmaf_rn(-t, __fmaf_rn(r, r, -q), __fmaf_rn(-t, q, 1.0f));
-  const int up = max(-149, min(127, f - k));
-  return {exp2_float(up), __fmul_rn(__fmaf_rn(0.5f * r, d, r), exp2_float(f - k - up))};
+  const int up = max(-149, min(127, f - k - 1));
+  const float rest = 2.0f * exp2_float(f - k - 1 - up), hi = __fmaf_rn(0.5f * r, d, r);
+  return {exp2_float(up), hi * rest, __fmaf_rn(0.5f * r, d, r - hi) * rest};
 }
 
 // Sum over the CTA of (h x)^2, h the row's values from memory.  Out of line, for the few rows that
@@ -352,7 +373,7 @@ template <int FMT, int U, int PHASE>
 __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a, const RowOutput o) {
   __shared__ float sums[2][32];
   __shared__ uint32_t maxima[32];
-  __shared__ float cta_max;
+  __shared__ unsigned long long cta_max;
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t units = a.cols / kUnit;
@@ -416,14 +437,14 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
   const InvRms inv = row_inv_rms(a, s, sums, add ? a.residual_out + r * a.ld_res_out : src, row ? a.cols : 0);
 #pragma unroll
   for (int k = 0; k < U; ++k) as_words(h[k]);
-  const uint64_t up = pack2(inv.up, inv.up), rstd = pack2(inv.r, inv.r), one = pack2(1.0f, 1.0f);
-  const uint64_t offset = pack2(a.weight_offset, a.weight_offset);
+  const uint64_t up = pack2(inv.up, inv.up), rstd = pack2(inv.r, inv.r), rstd_lo = pack2(inv.r_lo, inv.r_lo);
+  const uint64_t one = pack2(1.0f, 1.0f), offset = pack2(a.weight_offset, a.weight_offset);
 
-  auto values = [&](int k, float (&v)[16]) {
+  // (h up)(weight + offset) of unit k
+  auto weighted = [&](int k, uint64_t (&x)[8]) {
     const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
-    uint64_t x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(pack2(bf16_lo(h[k][i]), bf16_hi(h[k][i])), up), rstd);
+    for (int i = 0; i < 8; ++i) x[i] = mul2(pack2(bf16_lo(h[k][i]), bf16_hi(h[k][i])), up);
     if (a.weight != nullptr && u < units) {
       uint32_t w[8];
 #pragma unroll
@@ -434,8 +455,6 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], fma2(pack2(bf16_lo(w[i]), bf16_hi(w[i])), one, offset));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) unpack2(x[i], v[2 * i], v[2 * i + 1]);
   };
 
   float sg = 1.0f;
@@ -443,18 +462,22 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
     float m = 0.0f;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
+      uint64_t x[8];
       float v[16];
-      values(k, v);
+      weighted(k, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) unpack2(x[i], v[2 * i], v[2 * i + 1]);
       if (row && threadIdx.x + static_cast<int64_t>(k) * T < units) m = max_nan(m, amax16(v));
     }
-    m = block_max(m, maxima);
+    // the row's largest |v| in binary64: the tensor scale moves every rounding border of the output
+    const double amax = row ? block_max(m, maxima) * (static_cast<double>(inv.r) + inv.r_lo) : 0.0;
     if constexpr (PHASE == kAmax) {
-      if (threadIdx.x == 0 && __float_as_uint(m) != 0u) atomicMax(o.amax_word, __float_as_uint(m));
+      if (threadIdx.x == 0) publish_amax(amax, o.amax_word);
       return;
     }
-    sg = tensor_scale(cluster_max(m, &cta_max));
+    sg = tensor_scale(cluster_max(amax, &cta_max));
   } else if constexpr (FMT == NVFP4_OUT_NVFP4) {
-    sg = PHASE == kFormat ? tensor_scale(__uint_as_float(*o.amax_word)) : *o.gs_in;
+    sg = PHASE == kFormat ? tensor_scale(__longlong_as_double(*o.amax_word)) : *o.gs_in;
   }
   if (FMT == NVFP4_OUT_NVFP4 && o.gs_out && blockIdx.x == 0 && threadIdx.x == 0) *o.gs_out = sg;
   if (row) {
@@ -462,8 +485,13 @@ __global__ void __launch_bounds__(norm_threads(U)) norm_kernel(const NormArgs a,
     for (int k = 0; k < U; ++k) {
       const int64_t u = threadIdx.x + static_cast<int64_t>(k) * T;
       if (U > 1 && u - threadIdx.x >= units) break;
+      uint64_t x[8];
       float v[16];
-      values(k, v);
+      weighted(k, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        unpack2(FMT == NVFP4_OUT_BF16 ? mul2(x[i], rstd) : fma2(x[i], rstd, mul2(x[i], rstd_lo)), v[2 * i],
+                v[2 * i + 1]);
       emit<FMT>(v, r, u, u < units, a.cols, sg, o);
     }
   }
@@ -493,9 +521,9 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_
     return bf16_bits_to_float(h);
   };
   auto finish = [&](int64_t c, float f, InvRms inv) {
-    float v = __fmul_rn(__fmul_rn(f, inv.up), inv.r);
+    float v = __fmul_rn(f, inv.up);
     if (a.weight) v = __fmul_rn(v, __fadd_rn(bf16_bits_to_float(a.weight[c]), a.weight_offset));
-    out[r * ld_out + c] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+    out[r * ld_out + c] = static_cast<uint16_t>(pack_bf16(__fmul_rn(v, inv.r), 0.0f));
   };
   if constexpr (CACHED) {
     __shared__ float sums[2][32];
@@ -621,14 +649,13 @@ __global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint1
     uint32_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float lo = __fmul_rn(__fmul_rn(bf16_lo(h[k][i]), inv.up), inv.r);
-      float hi = __fmul_rn(__fmul_rn(bf16_hi(h[k][i]), inv.up), inv.r);
+      float lo = __fmul_rn(bf16_lo(h[k][i]), inv.up), hi = __fmul_rn(bf16_hi(h[k][i]), inv.up);
       if (a.weight != nullptr) {
         const uint32_t ww = c0 & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
         lo = __fmul_rn(lo, __fadd_rn(bf16_lo(ww), a.weight_offset));
         hi = __fmul_rn(hi, __fadd_rn(bf16_hi(ww), a.weight_offset));
       }
-      y[i] = pack_bf16(lo, hi);
+      y[i] = pack_bf16(__fmul_rn(lo, inv.r), __fmul_rn(hi, inv.r));
     }
     store(out, j, y);
   }
@@ -692,7 +719,7 @@ constexpr int gate_ctas(int fmt, int phase) { return fmt == NVFP4_OUT_NVFP4 && p
 template <int FMT, int PHASE>
 __global__ void __launch_bounds__(kGateThreads, gate_ctas(FMT, PHASE)) gate_kernel(const GateArgs a, const RowOutput o) {
   __shared__ uint32_t maxima[32];
-  __shared__ float cta_max;
+  __shared__ unsigned long long cta_max;
   grid_dependency_wait();
   grid_dependents_launch();
   const int rows = static_cast<int>(a.rows), units = static_cast<int>(a.cols / kUnit), chunks = (units + 31) / 32;
@@ -754,12 +781,12 @@ __global__ void __launch_bounds__(kGateThreads, gate_ctas(FMT, PHASE)) gate_kern
     each(false, [&](int, int, bool, const float(&v)[16]) { m = max_nan(m, amax16(v)); });
     m = block_max(m, maxima);
     if constexpr (PHASE == kAmax) {
-      if (threadIdx.x == 0 && __float_as_uint(m) != 0u) atomicMax(o.amax_word, __float_as_uint(m));
+      if (threadIdx.x == 0) publish_amax(m, o.amax_word);
       return;
     }
     sg = tensor_scale(cluster_max(m, &cta_max));
   } else if constexpr (FMT == NVFP4_OUT_NVFP4) {
-    sg = PHASE == kFormat ? tensor_scale(__uint_as_float(*o.amax_word)) : *o.gs_in;
+    sg = PHASE == kFormat ? tensor_scale(__longlong_as_double(*o.amax_word)) : *o.gs_in;
   }
   if (FMT == NVFP4_OUT_NVFP4 && o.gs_out && blockIdx.x == 0 && threadIdx.x == 0) *o.gs_out = sg;
   // the second launch walks backwards: the end of the first's reads is in L2
@@ -913,7 +940,7 @@ cudaError_t launch_rms_norm(const NormArgs& args, const RowOutput& output, int* 
   }
   if (o.gs_in) return norm_launch_u<NVFP4_OUT_NVFP4, kOnePass>(a, o, launches, stream);
   if (a.rows <= kCluster) return norm_launch_u<NVFP4_OUT_NVFP4, kCluster1>(a, o, launches, stream);
-  cudaError_t e = cudaMemsetAsync(o.amax_word, 0, sizeof(uint32_t), stream);
+  cudaError_t e = cudaMemsetAsync(o.amax_word, 0, sizeof(*o.amax_word), stream);
   if (e == cudaSuccess) e = norm_launch_u<NVFP4_OUT_NVFP4, kAmax>(a, o, launches, stream);
   if (e == cudaSuccess) e = norm_launch_u<NVFP4_OUT_NVFP4, kFormat>(a, o, launches, stream);
   return e;
@@ -952,7 +979,7 @@ cudaError_t launch_silu_mul(const GateArgs& args, const RowOutput& output, int* 
   if (o.gs_in) return gate_launch<NVFP4_OUT_NVFP4, kOnePass>(a, o, launches, stream);
   // a small output: one cluster computes the amax and formats
   if (a.rows * a.cols <= kClusterMax) return gate_launch<NVFP4_OUT_NVFP4, kCluster1>(a, o, launches, stream);
-  cudaError_t e = cudaMemsetAsync(o.amax_word, 0, sizeof(uint32_t), stream);
+  cudaError_t e = cudaMemsetAsync(o.amax_word, 0, sizeof(*o.amax_word), stream);
   if (e == cudaSuccess) e = gate_launch<NVFP4_OUT_NVFP4, kAmax>(a, o, launches, stream);
   if (e == cudaSuccess) e = gate_launch<NVFP4_OUT_NVFP4, kFormat>(a, o, launches, stream);
   return e;
