@@ -43,3 +43,34 @@ def test_norm_of_a_row_whose_sum_of_squares_passes_binary32(cuda_device):
     """4096 values of 4e17: their mean square is 1.6e35, their sum 6.6e38."""
     x = torch.full((3, 4096), 4e17, dtype=torch.bfloat16, device="cuda")
     assert (nv.rms_norm(x) == 1.0).all()
+
+
+@pytest.mark.parametrize("cols", [512, 333])                 # 16-value units, one value at a time
+def test_gate_of_far_negative_values(cuda_device, cols):
+    """e^-g passes binary32 from g = -88.7 on, where a large up value still brings the product back into range."""
+    g = torch.linspace(-78.0, -185.0, 64, device="cuda")[:, None].expand(64, cols)
+    u = torch.ldexp(bf16((64, cols), 1).float().clamp(-3.9, 3.9), torch.arange(cols, device="cuda") % 126).to(torch.bfloat16)
+    g = g.to(torch.bfloat16).contiguous()
+    v = ref.gate64(g, u)
+    assert (np.abs(v) < 3e38).all() and (np.abs(v) > 1e-20).mean() > 0.1
+    ref.check_bf16(nv.silu_mul(g, u), v, ref.GATE_DELTA)
+    if cols % 32 == 0:
+        ref.check_blocks(nv.silu_mul(g, u, out_format="mxfp8", layout="linear"), v, "mxfp8", "linear", ref.GATE_DELTA)
+
+
+def test_gated_product_of_far_negative_gates(cuda_device):
+    """The same behind the products: a gate of -99 (the quantized -1 times 96) and an up product of 2^126."""
+    K = 32
+    def weight(value):                                       # N = 16 rows of one value, exact in NVFP4
+        w = torch.zeros((16, K), dtype=torch.bfloat16, device="cuda")
+        w[:, 0] = value
+        return nv.nvfp4_quantize(w, global_scale=torch.ones(1, device="cuda"))
+    x = torch.zeros((2, K), dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[1, 0] = 96.0, 2.0 ** 5
+    gate, up = weight(-1.0), weight(6.0)
+    up.global_scale.fill_(2.0 ** 117)
+    y, _ = ref.matvec64(x, up, gate)
+    assert np.abs(y[0]).min() > 1e-4 and np.isfinite(y).all()
+    # one product per sum: the gate is off by 3 roundings, so e^gate by 99 * 3 * 2^-24, and BF16 by half a step
+    got = nv.matvec(x, up, gate).double().cpu().numpy()
+    assert (np.abs(got - y) <= np.abs(y) * (2.0 ** -8 + 2.0 ** -14)).all()

@@ -35,6 +35,7 @@
 
 #include "layer_ops.h"
 #include "ptx.cuh"
+#include "silu.cuh"
 
 namespace nvfp4 {
 
@@ -647,8 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       for (int k = 0; k < 4; ++k) {
         float f = ss[k] * sw;
         if (GATED) {
-          const float gt = ss[k] * sgate;
-          f = gt / (1.0f + expf(-gt)) * (vv[k] * sw);
+          f = silu_times(ss[k] * sgate, vv[k] * sw);
         }
         if (row + 32 * k < N) y[32 * k] = static_cast<uint16_t>(pack_bf16(f, 0.0f));
       }

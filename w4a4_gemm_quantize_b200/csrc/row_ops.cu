@@ -22,6 +22,7 @@
 #include "layer_ops.h"
 #include "ptx.cuh"
 #include "quant_block.cuh"
+#include "silu.cuh"
 
 namespace nvfp4 {
 
@@ -307,10 +308,6 @@ __device__ __forceinline__ float block_max(float m, uint32_t* part) {
 struct InvRms {
   float up, r, r_lo;
 };
-
-__device__ __forceinline__ float exp2_float(int k) {  // k in [-149, 127]
-  return __int_as_float(k >= -126 ? (k + 127) << 23 : 1 << (k + 149));
-}
 
 // From m = (mean square + eps) 4^f.  With m = 4^k t, t in [1, 4): r = 2 / sqrt(t) by the function
 // and one Newton step, r + r (1 - t (r / 2)^2) / 2, whose residual takes the square in two floats.
@@ -661,12 +658,7 @@ __global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint1
   }
 }
 
-// g / (1 + e^-g) * u of one value, by IEEE operations: the tails, infinities and NaN.
-__device__ __forceinline__ float silu_times(float g, float u) {
-  return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
-}
-
-// The same of the sixteen values of a unit, two to a packed instruction, for |g| < 80.
+// silu_times of the sixteen values of a unit, two to a packed instruction, for |g| < 80.
 //   e^-g = 2^h (1 + l ln 2), h = RN(-g log2 e), l what h leaves of -g log2 e, with the second
 //   word of log2 e; d = 1 + e^-g; 1 / d by the approximate reciprocal and one Newton step.
 // The error stays near one unit in the last place, so the block formats' rounding borders see
