@@ -621,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     constexpr int kOut = GATED ? 2 : 4;  // lines of a 16-row group
     const int outputs = nt * R * kOut * M;
     const int out_line = lane % kOut;
-    // sums of output i over the warps that had a part of its tile (gated: both products), the
-    // token's scaling undone
+    // sums of output i over the warps that had a part of its tile (gated: both products), under the
+    // tensor scale, then the token's scaling undone: y / s_g, often 2^15 times y, may have no binary32
     auto sum = [&](int i, float4& s, float4& v) {
       const int tr = div_m(p, i / kOut), m = i / kOut - tr * M, ti = tr / R;
       const int w0 = first[ti], w1 = last[ti];
@@ -635,8 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
         if (GATED) v = add4(v, *reinterpret_cast<const float4*>(q + 8));
       }
       const float up = exp2_int(down_exponent(top[m]));
-      s = make_float4(s.x * up, s.y * up, s.z * up, s.w * up);
-      if (GATED) v = make_float4(v.x * up, v.y * up, v.z * up, v.w * up);
+      const float s0 = GATED ? sgate : sw;
+      s = make_float4(s.x * s0 * up, s.y * s0 * up, s.z * s0 * up, s.w * s0 * up);
+      if (GATED) v = make_float4(v.x * sw * up, v.y * sw * up, v.z * sw * up, v.w * sw * up);
     };
     auto write = [&](int i, float4 s, float4 v) {
       const int tr = div_m(p, i / kOut), m = i / kOut - tr * M;
@@ -646,10 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       const float ss[4] = {s.x, s.y, s.z, s.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float f = ss[k] * sw;
-        if (GATED) {
-          f = silu_times(ss[k] * sgate, vv[k] * sw);
-        }
+        const float f = GATED ? silu_times(ss[k], vv[k]) : ss[k];
         if (row + 32 * k < N) y[32 * k] = static_cast<uint16_t>(pack_bf16(f, 0.0f));
       }
     };
