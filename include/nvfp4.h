@@ -357,9 +357,9 @@ nvfp4_status nvfp4_silu_mul(const void *gate, int64_t ld_gate, const void *up, i
  *   out          device BF16, M x N, row stride ld_out >= N (2-byte aligned, any stride);
  *                it must not overlap an input (INVALID_ARG).
  *   0 <= M <= 16, 1 <= N <= 2^30, 32 <= K <= 2^19, K % 32 == 0.
- * FP32 accumulation, no workspace, the same bits on every call.  Weights are exact; x is
- * exact down to 2^-21 of the largest finite magnitude of its token (in the part of K that
- * a CTA handles), below that rounded at 2^-32 of it.
+ * FP32 accumulation, no workspace, the same bits on every call.  Weights and x are exact
+ * (MXFP8 values below 2^-133 are rounded there); where nonzero values of one token lie more
+ * than 30 binades apart the call takes up to half as long again.
  * Errors: INVALID_ARG, SHAPE, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA. */
 nvfp4_status nvfp4_matvec(const void *x, const uint8_t *x_scales, nvfp4_sf_layout x_layout, int64_t M, int64_t K,
                           int64_t ld_x, const uint8_t *w_codes, const uint8_t *w_scales,
