@@ -412,6 +412,13 @@ nvfp4_status nvfp4_quantize_noalloc(const void *x, int64_t rows, int64_t cols, i
                                     const float *global_scale_in, uint8_t *codes, uint8_t *scales,
                                     float *global_scale_out, float *block_err, void *stream);
 
+/* How nvfp4_matvec (mxfp4_weights 0) or mxfp4_matvec cuts a call of these sizes, for tests and
+ * tuning; host side only.  plan[0]: CTAs of a cluster that share K (1: none do); plan[1]:
+ * batches of tiles per CTA at most; plan[2]: 1 where a cluster's sums take the place of x in
+ * shared memory (all of the first launch); plan[3]: launches.
+ * Errors: INVALID_ARG, SHAPE. */
+nvfp4_status nvfp4_matvec_plan(int64_t M, int64_t N, int64_t K, int mxfp4_weights, int gated, int32_t plan[4]);
+
 /* Number of kernels the most recent nvfp4_quantize / nvfp4_dequantize /
  * nvfp4_gemm / nvfp4_rms_norm / nvfp4_silu_mul / nvfp4_matvec / mxfp4_matvec call
  * on the calling host thread enqueued (library bookkeeping for launch counting; no

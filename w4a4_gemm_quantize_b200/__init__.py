@@ -72,6 +72,7 @@ SIGNATURES = {
     "nvfp4_silu_mul": ([_P, _I64, _P, _I64, _I64, _I64, _I, _I, _P, _P, _I64, _P, _P, _P, _SZ, _P], _I),
     "nvfp4_matvec": ([_P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _P], _I),
     "mxfp4_matvec": ([_P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P], _I),
+    "nvfp4_matvec_plan": ([_I64, _I64, _I64, _I, _I, ctypes.POINTER(ctypes.c_int32)], _I),
     "nvfp4_read_device_error": ([_P, _P, ctypes.POINTER(ctypes.c_uint32)], _I),
     "nvfp4_last_launch_count": ([], _I),
     "nvfp4_quantize_noalloc": ([_P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P], _I),
@@ -611,6 +612,14 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
     if st:
         _check(st, "nvfp4_matvec" if nvfp4 else "mxfp4_matvec")
     return out
+
+
+def matvec_plan(M: int, N: int, K: int, mxfp4_weights: bool = False, gated: bool = False):
+    """How matvec cuts a call of these sizes: (CTAs that share K, batches of tiles per CTA, whether a cluster's sums
+    take x's place in shared memory, launches); see nvfp4_matvec_plan in include/nvfp4.h."""
+    plan = (ctypes.c_int32 * 4)()
+    _check(load_library().nvfp4_matvec_plan(M, N, K, int(mxfp4_weights), int(gated), plan), "nvfp4_matvec_plan")
+    return plan[0], plan[1], bool(plan[2]), plan[3]
 
 
 def mxfp8_scales_bytes(rows: int, cols: int, layout=SF_SWIZZLED) -> int:

@@ -250,4 +250,18 @@ nvfp4_status mxfp4_matvec(const void* x, const uint8_t* x_scales, nvfp4_sf_layou
                 true, N, out, ld_out, stream);
 }
 
+nvfp4_status nvfp4_matvec_plan(int64_t M, int64_t N, int64_t K, int mxfp4_weights, int gated, int32_t plan[4]) {
+  if (!plan || M < 1 || N < 1 || K < 1) return NVFP4_ERR_INVALID_ARG;
+  if (K % 32 != 0 || M > nvfp4::kMatvecMaxTokens || N > kMaxRows || K > (int64_t{1} << 19)) return NVFP4_ERR_SHAPE;
+  nvfp4::MatvecArgs a{};
+  static const uint8_t some = 0;  // (only told from null)
+  a.mx = mxfp4_weights != 0;
+  if (gated) a.gate.codes = &some;
+  a.M = static_cast<int>(M), a.N = N, a.K = K;
+  nvfp4::MatvecPlan p;
+  if (!nvfp4::plan_matvec(a, &p)) return NVFP4_ERR_SHAPE;
+  plan[0] = p.split, plan[1] = p.batches, plan[2] = p.sums_over_x, plan[3] = p.launches;
+  return NVFP4_OK;
+}
+
 }  // extern "C"

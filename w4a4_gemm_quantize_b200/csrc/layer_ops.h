@@ -72,6 +72,16 @@ struct MatvecArgs {
 
 constexpr int kMatvecMaxTokens = 16;
 
+// How a call is cut (host side only; pointers tell BF16, gate and format, and are not read): CTAs of a
+// cluster that share K, batches of tiles per CTA at most, whether a cluster's sums take x's place
+// in shared memory -- of the first launch -- and the launches.  False: it fits no launch.
+struct MatvecPlan {
+  int split, batches;
+  bool sums_over_x;
+  int launches;
+};
+bool plan_matvec(const MatvecArgs& a, MatvecPlan* plan);
+
 // One launch, or several when x of so many tokens does not fit shared memory.
 cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t stream);
 

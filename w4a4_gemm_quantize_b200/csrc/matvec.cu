@@ -918,25 +918,34 @@ Plan plan(int M, int x_units, int tiles, int split, size_t ring, int R) {
 
 }  // namespace
 
-cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t stream) {
-  Params p{};
+namespace {
+
+// The launch of so many tokens: whether x of them fits any split, then its shape and parameters.
+struct Launch {
+  Params p;
+  Shape shape;
+  int groups;
+  size_t smem;
+};
+
+bool prepare(const MatvecArgs& a, Launch& l) {
+  l = {};
+  Params& p = l.p;
   p.a = a;
   const bool gated = a.gate.codes != nullptr;
-  const Shape shape = a.M > 8 ? kPaired : a.K % 64 == 0 ? kWide : kNarrow;
-  const int R = shape == kPaired ? 2 : 1;
+  l.shape = a.M > 8 ? kPaired : a.K % 64 == 0 ? kWide : kNarrow;
+  const int R = l.shape == kPaired ? 2 : 1;
   const int64_t tail = a.N % 128;
   const int lines_per_tile = (gated ? 2 : 4) * R;
   const int64_t lines = a.N / 128 * 32 + (tail < 32 ? tail : 32);  // neighbour lines, 4 rows each
   p.tiles = static_cast<int>((lines + lines_per_tile - 1) / lines_per_tile);
   p.units = static_cast<int>((a.K + kUnit - 1) / kUnit);
   p.atoms = static_cast<int>((a.K / (a.mx ? 32 : 16) + 3) / 4);
-  const size_t ring = a.mx ? ring_bytes<true>(shape) : ring_bytes<false>(shape);
+  const size_t ring = a.mx ? ring_bytes<true>(l.shape) : ring_bytes<false>(l.shape);
   // CTAs per cluster: the fewest items for the busiest CTA among the splits whose part of x
   // fits.  Clusters that the GPU holds at a time, of CTAs that fill an SM: 148, 74, 33, 15.
   static const int kSplits[4] = {1, 2, 4, 8}, kGroups[4] = {148, 74, 33, 15};
   int64_t best = -1;
-  int groups = 1;
-  size_t smem = 0;
   for (int i = 0; i < 4; ++i) {
     const int s = kSplits[i], n = p.tiles < kGroups[i] ? p.tiles : kGroups[i];
     const int x_units = (p.units + s - 1) / s, tiles = (p.tiles + n - 1) / n;
@@ -950,12 +959,40 @@ cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t strea
     p.split = s;
     p.batch = q.tiles;
     p.x_units = x_units;
-    groups = n;
-    smem = q.smem;
+    l.groups = n;
+    l.smem = q.smem;
     p.sums_at = static_cast<int>(q.sums_at);
     p.sums_over_x = q.over_x;
   }
-  if (best < 0) {  // x of this many tokens fits no split: half of them at a time
+  if (best < 0) return false;
+  p.m_inv = static_cast<uint32_t>(((uint64_t{1} << 32) + a.M - 1) / a.M);
+  p.tiles_q = p.tiles / l.groups, p.tiles_r = p.tiles % l.groups;
+  p.units_q = p.units / p.split, p.units_r = p.units % p.split;
+  return true;
+}
+
+}  // namespace
+
+bool plan_matvec(const MatvecArgs& a, MatvecPlan* plan) {
+  Launch l;
+  if (!prepare(a, l)) {
+    if (a.M == 1) return false;
+    MatvecArgs first = a, second = a;
+    first.M = a.M / 2;
+    second.M = a.M - first.M;
+    MatvecPlan rest;
+    if (!plan_matvec(second, &rest) || !plan_matvec(first, plan)) return false;
+    plan->launches += rest.launches;
+    return true;
+  }
+  const int tiles = l.p.tiles_q + (l.p.tiles_r > 0);
+  *plan = {l.p.split, (tiles + l.p.batch - 1) / l.p.batch, l.p.sums_over_x, 1};
+  return true;
+}
+
+cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t stream) {
+  Launch l;
+  if (!prepare(a, l)) {  // x of this many tokens fits no split: half of them at a time
     if (a.M == 1) return cudaErrorInvalidValue;
     MatvecArgs first = a, second = a;
     first.M = a.M / 2;
@@ -967,15 +1004,13 @@ cudaError_t launch_matvec(const MatvecArgs& a, int* launches, cudaStream_t strea
     const cudaError_t e = launch_matvec(first, launches, stream);
     return e != cudaSuccess ? e : launch_matvec(second, launches, stream);
   }
-  p.m_inv = static_cast<uint32_t>(((uint64_t{1} << 32) + a.M - 1) / a.M);
-  p.tiles_q = p.tiles / groups, p.tiles_r = p.tiles % groups;
-  p.units_q = p.units / p.split, p.units_r = p.units % p.split;
-  const int grid = groups * p.split;
+  const int grid = l.groups * l.p.split;
   ++*launches;
-  if (a.mx) return gated ? launch_format<true, true>(p, shape, grid, smem, stream)
-                         : launch_format<true, false>(p, shape, grid, smem, stream);
-  return gated ? launch_format<false, true>(p, shape, grid, smem, stream)
-               : launch_format<false, false>(p, shape, grid, smem, stream);
+  const bool gated = a.gate.codes != nullptr;
+  if (a.mx) return gated ? launch_format<true, true>(l.p, l.shape, grid, l.smem, stream)
+                         : launch_format<true, false>(l.p, l.shape, grid, l.smem, stream);
+  return gated ? launch_format<false, true>(l.p, l.shape, grid, l.smem, stream)
+               : launch_format<false, false>(l.p, l.shape, grid, l.smem, stream);
 }
 
 }  // namespace nvfp4
