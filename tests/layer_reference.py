@@ -146,9 +146,11 @@ def dequantize64(w):
 
 def matvec64(x, w, gate=None):
     """(y, bound): y = x w^T (gated: silu(x gate^T) * it) in 64 bits on the GPU, and the error allowed before the
-    BF16 rounding: binary32 accumulation.  A warp adds at most 12 slices x 8 mma of its K share, each off by at
-    most 2^-22 of the sum of magnitudes S (operand alignment inside the mma included), 16 partial sums and the
-    slices' sums follow: under 2^-14 S."""
+    BF16 rounding: binary32 accumulation, 2^-14 of the sum of magnitudes S.  By operation count: a warp keeps a tile's
+    sums over its part of K, a chain of at most K / 16 mma, each off by at most 2^-22 of S (operand alignment inside
+    the mma included); 16 warps' and 8 CTAs' sums follow: (K / 16 + 24) 2^-22 S, which is 2^-14 S up to K = 3700.
+    Longer rows are held to the same 2^-14, tighter than their count: the partial sums stay far below S and their
+    roundings have both signs (the largest excess over half a BF16 step, K up to 524288, was 2^-26 S)."""
     x = x.double().cuda()
 
     def product(q):

@@ -58,7 +58,7 @@ def test_every_way_of_cutting_a_call(cuda_device, M, N, K, kind, gated):
     for x in (near.to(torch.bfloat16), far.to(torch.bfloat16)):
         got = nv.matvec(x, w, gate)
         y, s = product(x, rows, N)
-        bound = s * 2.0 ** -14
+        bound = s * 2.0 ** -14                                         # as layer_reference.matvec64 has it
         if gated:
             z, sz = product(x, gate_rows, N)
             e = z / (1.0 + torch.exp(-z))
