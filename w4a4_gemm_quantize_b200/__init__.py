@@ -421,6 +421,19 @@ def _like(t: torch.Tensor, name: str, dtype, numel: int, like: torch.Tensor) -> 
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {like.device}")
 
 
+def _weight(t, dev: int) -> None:
+    """Checks that a 4-bit weight's tensors are those of its stated size, one byte to a code pair and to a block scale,
+    and on device `dev`."""
+    nvfp4, c, s = isinstance(t, NVFP4Tensor), t.codes, t.scales
+    if c.get_device() != dev or s.get_device() != dev or (nvfp4 and t.global_scale.get_device() != dev):
+        raise ValueError(f"the weights must be on x's device, cuda:{dev}")
+    if (c.numel() != t.rows * (t.cols // 2) or s.numel() != _swizzled_bytes(t.rows, t.cols // (16 if nvfp4 else 32))
+            or c.element_size() != 1 or s.element_size() != 1 or not c.is_contiguous() or not s.is_contiguous()):
+        raise ValueError(f"a weight's codes or scales are not those of a {t.rows} x {t.cols} tensor")
+    if nvfp4 and (t.global_scale.dtype is not torch.float32 or t.global_scale.numel() != 1):
+        raise ValueError("a weight's global_scale must be one float32")
+
+
 def _swizzled_bytes(rows: int, blocks: int) -> int:
     """nvfp4_scales_bytes / mxfp4_scales_bytes of the SWIZZLED layout."""
     return (rows + 127) // 128 * 128 * ((blocks + 3) // 4 * 4)
@@ -582,15 +595,10 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
     if not nvfp4 and not isinstance(w, MXFP4Tensor):
         raise ValueError("w must be an NVFP4Tensor or an MXFP4Tensor")
     N, dev = w.rows, data.get_device()
-    codes_n, scales_n = N * (K // 2), _swizzled_bytes(N, K // (16 if nvfp4 else 32))
     for t in (w,) if w_gate is None else (w, w_gate):
         if type(t) is not type(w) or t.rows != N or t.cols != K or t.layout != SF_SWIZZLED:
             raise ValueError("the weights must share K with x, one kind and shape, and have swizzled scales")
-        c, s = t.codes, t.scales
-        if c.get_device() != dev or s.get_device() != dev or (nvfp4 and t.global_scale.get_device() != dev):
-            raise ValueError(f"the weights must be on {data.device}")
-        if c.numel() != codes_n or s.numel() != scales_n or not c.is_contiguous() or not s.is_contiguous():
-            raise ValueError(f"a weight's codes or scales are not those of a {N} x {K} tensor")
+        _weight(t, dev)
     if stream is not None or dev != _current_device():
         with _On(data.device, stream):
             return matvec(x, w, w_gate, out)
