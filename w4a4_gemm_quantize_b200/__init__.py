@@ -110,9 +110,16 @@ def _check(status: int, where: str):
         raise Nvfp4Error(status, where)
 
 
+# What torch.cuda.current_device and current_stream ask, without their host time (a few microseconds a call); a
+# torch that lacks these names has the public calls.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -391,11 +398,6 @@ class _On:
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
             c.__exit__(*exc)
-
-
-# what torch.cuda.current_device and current_stream ask, without their host time (a few microseconds a call)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _ld(t: torch.Tensor, name: str, shape=None, dev: int = -1) -> int:
