@@ -304,7 +304,7 @@ size_t nvfp4_row_workspace_bytes(void);
  *   h = BF16(x + residual)  (h = x without a residual), stored to residual_out;
  *   v = h (weight + weight_offset) r,  r = 1 / sqrt(mean over the row of h^2 + eps),
  * sums and v in FP32 (the product before r: exact for a BF16 factor; NVFP4's computed scale
- * from v in FP64).  The norm sees the rounded h, the value that the residual stream
+ * from the largest product times r in FP64).  The norm sees the rounded h, the value that the residual stream
  * keeps, so the call equals an addition in BF16 followed by a norm.  Rows of any finite
  * magnitude are normalised, also where their squares leave FP32's range; one with a NaN or
  * an infinity, or of zeros under eps 0, follows the formula.
@@ -315,8 +315,9 @@ size_t nvfp4_row_workspace_bytes(void);
  *   weight       device, BF16, cols values, or NULL (ones, and weight_offset is not used).
  *   weight_offset added to the weight in FP32 (1 for checkpoints that store weight - 1).
  *   eps          finite, >= 0.
- *   out          v in out_format (see there); BF16 may be written over x or residual_out's
- *                input x (same pointer and stride).  ld_out is read for BF16 only.
+ *   out          v in out_format (see there); BF16 may be written over x, or over residual
+ *                where residual_out is elsewhere (same pointer and stride).  ld_out is read
+ *                for BF16 only.
  *   layout, scales  the block formats' scales; NULL for BF16.
  *   global_scale_in  NVFP4: device float > 0, the result's tensor scale, or NULL: amax / 2688
  *                of v, computed on the device (1 for an all-zero result).  NULL otherwise.
@@ -357,9 +358,9 @@ nvfp4_status nvfp4_silu_mul(const void *gate, int64_t ld_gate, const void *up, i
  *   out          device BF16, M x N, row stride ld_out >= N (2-byte aligned, any stride);
  *                it must not overlap an input (INVALID_ARG).
  *   0 <= M <= 16, 1 <= N <= 2^30, 32 <= K <= 2^19, K % 32 == 0.
- * FP32 accumulation, no workspace, the same bits on every call.  Weights and x are exact
- * (MXFP8 values below 2^-133 are rounded there); where nonzero values of one token lie more
- * than 30 binades apart the call takes up to half as long again.
+ * FP32 accumulation, no workspace, the same bits on every call.  Weights and x are exact;
+ * where nonzero values of one token lie more than 30 binades apart, the weights are gone over
+ * once more for each 30 binades that hold some.
  * Errors: INVALID_ARG, SHAPE, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA. */
 nvfp4_status nvfp4_matvec(const void *x, const uint8_t *x_scales, nvfp4_sf_layout x_layout, int64_t M, int64_t K,
                           int64_t ld_x, const uint8_t *w_codes, const uint8_t *w_scales,

@@ -16,6 +16,7 @@ def weight(N, K, kind, g):
     """Any codes, block scales over a few binades; their values (64 bits) row by row in `rows`."""
     block = 16 if kind == "nvfp4" else 32
     codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    codes[:, :8] = 0                                                   # 16 columns of zeros, for x's large values
     nblk = K // block
     low, high = (0x30, 0x48) if kind == "nvfp4" else (118, 126)
     lin = torch.randint(low, high, (N, nblk), generator=g, device="cuda", dtype=torch.uint8)
@@ -53,9 +54,10 @@ def test_every_way_of_cutting_a_call(cuda_device, M, N, K, kind, gated):
     w, rows = weight(N, K, kind, g)
     gate, gate_rows = weight(N, K, kind, g) if gated else (None, None)
     near = torch.randn((M, K), generator=g, device="cuda") * (0.02 if gated else 1.0)
-    far = near.clone()
-    far[:, ::2] *= 2.0 ** -40                                          # takes the BF16 form
-    for x in (near.to(torch.bfloat16), far.to(torch.bfloat16)):
+    far, last = near.clone(), near.clone()                             # more passes than one over the weights:
+    far[:, 16::2] *= 2.0 ** -40                                        # its first holds the result,
+    last[:, 3], last[1::2, 5] = 2.0 ** 90, 2.0 ** 45                   # its second, in odd tokens its third does
+    for x in (near.to(torch.bfloat16), far.to(torch.bfloat16), last.to(torch.bfloat16)):
         got = nv.matvec(x, w, gate)
         y, s = product(x, rows, N)
         bound = s * 2.0 ** -14                                         # as layer_reference.matvec64 has it

@@ -164,3 +164,20 @@ def test_tensor_scales_against_tokens(cuda_device, scale, power):
         y, bound = ref.matvec64(x, w)
         assert np.abs(y).max() < 3e38
         ref.check_product(nv.matvec(x, w), y, bound)
+
+
+def test_mxfp8_values_down_to_the_smallest(cuda_device):
+    """E4M3's smallest values under E8M0's smallest scales, 2^-136, beside large ones: exact like all others."""
+    N, K = 40, 96
+    w = nv.mxfp4_quantize(torch.ldexp(bf16((N, K), 1).float(), torch.full((), 90, device="cuda")).to(torch.bfloat16))
+    codes = torch.randint(1, 8, (2, K), device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)     # 2^-9 to 7 2^-9
+    for big in (0, 60, 134):
+        scales = torch.tensor([[big, 0, 1], [0, 2, big]], dtype=torch.uint8, device="cuda")
+        x = nv.MXFP8Tensor(codes, scales, 2, K, nv.SF_LINEAR)
+        y, bound = ref.matvec64(values(x), w)
+        ref.check_product(nv.matvec(x, w), y, bound)
+    zero_first = w.codes.clone()
+    zero_first[:, :16] = 0                                              # nothing but the smallest values is left
+    w0 = nv.MXFP4Tensor(zero_first, w.scales, N, K)
+    y, bound = ref.matvec64(values(x), w0)
+    ref.check_product(nv.matvec(x, w0), y, bound)

@@ -3,19 +3,18 @@
 //   y[m, n] = s_g sum_k x[m, k] q[n, k] s[n, k / G],  G = 16 (E4M3 s) or 32 (E8M0 s).
 //
 // Bound: the weight stream, N K (1/2 + 1/G) bytes from HBM; the products ride along on
-// mma.sync m16n8k16 (f16 or bf16 -> f32): 16 weight rows x 8 tokens, so up to 8 tokens need
+// mma.sync m16n8k16 (f16 x f16 -> f32): 16 weight rows x 8 tokens, so up to 8 tokens need
 // the mma of one (14336 x 4096 NVFP4: 9.0 us for 1 token, 12.1 for 8, 15.3 for 16).
 //
 // Exactness: an E2M1 code times an E4M3 scale has at most 6 significant bits and lies in
-// [2^-10, 2688], so NVFP4 weights are exact in binary16 and, under a power of two, in BF16.  E8M0
-// scales do not fit binary16; there the mma runs on the bare codes of one block and the binary32
-// partial product is multiplied by the block's power of two.  x becomes binary16 under a power of
-// two per token (over the part of K that a CTA handles), its largest finite magnitude just below
-// 2^15 (MXFP4 weights: 2^14); there it is exact down to 2^-31 (2^-30) of that largest one.  A CTA
-// whose part of x spans more than that -- a smaller value may be the only one that meets a weight
-// other than zero -- takes BF16 x and weights instead, whose codes cost twice the instructions to
-// decode (1 token, 14336 x 4096, all CTAs: 12.8 us instead of 9.0).  So x is exact too (E4M3 values from
-// 2^-133 on), and sums are binary32 throughout.
+// [2^-10, 2688], so NVFP4 weights are exact in binary16.  E8M0 scales do not fit binary16; there
+// the mma runs on the bare codes of one block and the binary32 partial product is multiplied by the
+// block's power of two.  x becomes binary16 under a power of two per token (over the part of K that
+// a CTA handles), its largest finite magnitude just below 2^15 (MXFP4 weights: 2^14); there it is
+// exact down to 2^-31 (2^-30) of that largest one.  Smaller values -- one may be the only one that
+// meets a weight other than zero -- are left out, and a CTA that has some goes over its weights
+// again for them, under their own power of two, until none is left.  So x is exact too, and sums
+// are binary32 throughout.
 //
 // Layout.  K is cut into chunks of 256 values (128 where K is no multiple of 64), N into
 // tiles of 16 rows: 4 neighbours in each of the 4 row quarters of a 128-row group, whose
@@ -47,7 +46,8 @@ namespace {
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kDepth = 2;        // weight items in flight per warp (3 and 4: no faster, less room for x)
 constexpr int kPad = 16;         // floats per token of a 16-row partial
-constexpr int kTokenWords = 5 * kMatvecMaxTokens + 4;
+constexpr int kTokenWords = 8 * kMatvecMaxTokens + 4;
+constexpr int kMaxPasses = 12;   // binary32 has 277 binades, a pass takes 30 at least
 constexpr int kUnit = 256;       // K is divided in units of this between a cluster's CTAs
 constexpr int kSmem = 226 * 1024;
 
@@ -109,19 +109,6 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// The eight E2M1 codes n_0 .. n_7 of a word times 2^-126 as four BF16 pairs (n_i, n_i+4): each
-// half of the word holds four codes, whose sign goes to bit 15 and the rest to bits 8 to 6.  Two
-// codes share a shift: their signs are picked from the word, the rest from the shifted word, and
-// four places further left the second code stands where the first did.
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&h)[4]) {
-  const uint32_t signs = 0x88008800u, code = 0x81C081C0u;
-  const uint32_t low = ((w << 2) & ~signs) | ((w << 8) & signs), high = ((w >> 6) & ~signs) | (w & signs);
-  h[0] = (low << 4) & code;
-  h[1] = low & code;
-  h[2] = (high << 4) & code;
-  h[3] = high & code;
-}
-
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -139,13 +126,6 @@ __device__ __forceinline__ int exponent(float s) { return max(-126, min(127, (__
 __device__ __forceinline__ float2 two_factors(float s, int k) {
   const int e = exponent(s), half = (e + k) / 2;
   return make_float2(s * exp2_float(-e) * exp2_float(half), exp2_float(e + k - half));
-}
-
-// BF16 sums are of x code scale 2^e, 2^e a tensor scale's power of two so far as BF16 has room for it
-// next to a block scale, and of x code 2^-8 for MXFP4, so that they leave binary32 no sooner than y.
-template <bool MX>
-__device__ __forceinline__ int bf16_exponent(float s) {
-  return MX ? -8 : max(-100, min(-9, exponent(s)));
 }
 
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
@@ -175,20 +155,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// d += a b, a 16 x 16 (rows of W), b 16 x 8 (tokens), in binary16 or BF16
-template <bool BF16>
+// d += a b, a 16 x 16 (rows of W), b 16 x 8 (tokens)
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  if constexpr (BF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // two E4M3 codes as floats
@@ -263,13 +236,22 @@ __device__ __forceinline__ int down_exponent(uint32_t top) {
   return top == 0u ? 0 : max(-126, static_cast<int>(top >> 23) - 126 - kTop<MX>);
 }
 
-// Scaled values from 2^L on are exact in binary16, whose last bit is 2^-24: BF16 has 8 bits, E4M3 4.
-__device__ __forceinline__ int low_exponent(bool mx8) { return mx8 ? -21 : -17; }
+// The bits of 2^(E + L), the lowest magnitude that is certain to be exact in binary16 after scaling, whose
+// last bit is 2^-24: BF16 has 8 bits, E4M3 4.  (No lower than 2^-126; below, both have fewer bits.)
+template <bool MX8>
+__device__ __forceinline__ uint32_t lowest(int E) {
+  return static_cast<uint32_t>(max(E + (MX8 ? -21 : -17) + 127, 1)) << 23;
+}
 
-// x in shared memory.  The part from unit u0 on (n units) of every token becomes mma fragments,
-// scaled binary16 or BF16 (in the pairs of codes_to_bf16()): 512 bytes per (unit, token), in which
-// place (j, t) of 16 bytes holds the 8 values that lane t of a quad multiplies with its word j of
-// the unit's codes.
+// The same without that lower end.
+__device__ __forceinline__ uint32_t lowest_exactly(bool mx8, int E) {
+  const int k = E + (mx8 ? -21 : -17);  // -147 at least
+  return k >= -126 ? static_cast<uint32_t>(k + 127) << 23 : 1u << (k + 149);
+}
+
+// x in shared memory.  The part from unit u0 on (n units) of every token becomes mma fragments
+// of scaled binary16: 512 bytes per (unit, token), in which place (j, t) of 16 bytes holds the 8
+// values that lane t of a quad multiplies with its word j of the unit's codes.
 // Odd tokens have the places of each pair j, j + 1 exchanged, so that two tokens' quads
 // read 8 different bank groups.  One warp per (unit, token), a lane per piece of 8 values.
 // fetch() copies the pieces as they come (E4M3: 8 bytes, then the word that holds their
@@ -334,6 +316,35 @@ struct Stager {
     return s;
   }
 
+  // The values of a piece; returns an MXFP8 piece's scale.
+  template <bool MX8>
+  __device__ __forceinline__ float values(uint4 v, int u, int m, float (&f)[8]) const {
+    if constexpr (MX8) {
+      return fp8(v, u, m, f);
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+      return 0.0f;
+    }
+  }
+
+  // This lane's place in a pair's 512 bytes.
+  __device__ __forceinline__ uint32_t place() const {
+    const int lane = threadIdx.x & 31;
+    const int j = MX ? lane >> 2 : WORDS == 8 ? lane & 7 : (lane >> 4) * 4 + (lane & 3);
+    const int t = MX ? lane & 3 : WORDS == 8 ? lane >> 3 : (lane >> 2) & 3;
+    return smem_u32(xs + j * 4 + t);
+  }
+  __device__ __forceinline__ void put(uint32_t place, int pair, int m, const float (&f)[8], float down) const {
+    st_shared16((place + pair * 512) ^ ((m & 1) << 6),
+                make_uint4(pack_half(f[0] * down, f[1] * down), pack_half(f[2] * down, f[3] * down),
+                           pack_half(f[4] * down, f[5] * down), pack_half(f[6] * down, f[7] * down)));
+  }
+
   // top: a zeroed word per token, receives the bits of its largest finite magnitude.
   template <bool MX8>
   __device__ __forceinline__ void find_top(uint32_t* top) const {
@@ -368,48 +379,57 @@ struct Stager {
     });
   }
 
-  // Every lane takes the pieces it copied; `top` gives the scaling of binary16.  Returns whether
-  // a value of the thread's is too small for that.
-  template <bool MX8, bool BF16>
+  // Every lane takes the pieces it copied and scales them by `top`.  Returns whether a value of the
+  // thread's is too small for that.
+  template <bool MX8>
   __device__ __forceinline__ bool stage(const uint32_t* top) const {
     bool far = false;
-    const int lane = threadIdx.x & 31;
-    const int j = MX ? lane >> 2 : WORDS == 8 ? lane & 7 : (lane >> 4) * 4 + (lane & 3);
-    const int t = MX ? lane & 3 : WORDS == 8 ? lane >> 3 : (lane >> 2) & 3;
-    const uint32_t place = smem_u32(xs + j * 4 + t);
+    const uint32_t to = place();
     each([&](int pair, int u, int m) {
       const uint4 v = *raw(pair);
       __syncwarp();  // the pair's pieces have been read: its 512 bytes may be written
-      float f[8], s = 0.0f;
-      if constexpr (MX8) {
-        s = fp8(v, u, m, f);
-      } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float f[8];
+      const float s = values<MX8>(v, u, m, f);
+      const int E = down_exponent<MX>(top[m]);
+      const uint32_t from = lowest<MX8>(E);
+      if (!MX8 || s * 0x1p-9f < __uint_as_float(from)) {  // (2^-9: the smallest E4M3 value but 0)
+        uint32_t least = 2u * from - 1u;                  // magnitudes as doubled bits less 1: a zero is the largest
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[2 * i] = __uint_as_float(w[i] << 16);
-          f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        for (int e = 0; e < 8; ++e) least = min(least, __float_as_uint(f[e]) * 2u - 1u);
+        far |= least < 2u * from - 1u;
       }
-      uint4 y;
-      if constexpr (BF16) {
-        y = make_uint4(pack_bf16(f[0], f[4]), pack_bf16(f[1], f[5]), pack_bf16(f[2], f[6]), pack_bf16(f[3], f[7]));
-      } else {
-        const int E = down_exponent<MX>(top[m]);
-        const float down = exp2_int(-E);
-        const uint32_t from = static_cast<uint32_t>(max(E + low_exponent(MX8) + 127, 1)) << 23;  // 2^(E + L)
-        if (!MX8 || s * 0x1p-9f < __uint_as_float(from)) {  // (2^-9: the smallest E4M3 value but 0)
-          uint32_t least = 2u * from - 1u;                  // magnitudes as doubled bits less 1: a zero is the largest
-#pragma unroll
-          for (int e = 0; e < 8; ++e) least = min(least, __float_as_uint(f[e]) * 2u - 1u);
-          far |= least < 2u * from - 1u;
-        }
-        y = make_uint4(pack_half(f[0] * down, f[1] * down), pack_half(f[2] * down, f[3] * down),
-                       pack_half(f[4] * down, f[5] * down), pack_half(f[6] * down, f[7] * down));
-      }
-      st_shared16((place + pair * 512) ^ ((m & 1) << 6), y);
+      put(to, pair, m, f, exp2_int(-E));
     });
     return far;
+  }
+
+  // The same of pieces fetched again and of the values below the token's limit[m] alone: those from
+  // there on and too small ones are left out (zeros), and next[m] (zeroed) receives the largest of
+  // the latter.
+  __device__ __forceinline__ void stage_below(bool mx8, const uint32_t* top, const uint32_t* limit,
+                                              uint32_t* next) const {
+    const uint32_t to = place();
+    each([&](int pair, int u, int m) {
+      const uint4 v = *raw(pair);
+      __syncwarp();
+      float f[8];
+      if (mx8)
+        values<true>(v, u, m, f);
+      else
+        values<false>(v, u, m, f);
+      const int E = down_exponent<MX>(top[m]);
+      const uint32_t from = lowest_exactly(mx8, E), end = limit[m];
+      uint32_t big = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+        if (b < min(from, end)) big = max(big, b);
+        f[e] = b < from || b >= end ? 0.0f : f[e];
+      }
+      big = __reduce_max_sync(0xFFFFFFFFu, big);
+      if (big != 0u && (threadIdx.x & 31) == 0) atomicMax(next + m, big);
+      put(to, pair, m, f, exp2_int(-E));
+    });
   }
 };
 
@@ -428,10 +448,8 @@ struct ItemBytes {
 
 // WORDS: 32-bit words of codes per lane and row of an item: 8 (chunks of 256) or 4 (128).
 // R: 16-row groups of a tile (2 only with WORDS 4: each word of x then serves two of them).
-// BF16: x and weights in BF16 instead of scaled binary16, by a CTA that found its x too wide for the
-// latter (it starts again, from the loads of x).  Returns whether it was.
-template <bool BF16, bool MX, int NT, bool GATED, int WORDS, int R>
-__device__ __forceinline__ bool matvec_body(const Params& p) {
+template <bool MX, int NT, bool GATED, int WORDS, int R>
+__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   using Ring = ItemBytes<MX, WORDS, R>;
   constexpr int kPerUnit = 8 / WORDS;              // chunks per unit
@@ -444,9 +462,13 @@ __device__ __forceinline__ bool matvec_body(const Params& p) {
   const int M = p.a.M, slot = M * kPad * R;
   const uint32_t ring = smem_u32(smem) + warp * kDepth * Ring::kBytes;
   uint4* xs = reinterpret_cast<uint4*>(smem + W * kDepth * Ring::kBytes);
-  // per token: largest magnitude; and one word: x too wide for binary16; then see below
+  // per token: largest magnitude; of one pass of many: the same of its values, the limit below which they
+  // lie, and the largest that it leaves out; what sums are multiplied by; and a word: x too wide for one pass
   uint32_t* top = reinterpret_cast<uint32_t*>(xs + p.x_units * M * 32);
-  float2* factors = reinterpret_cast<float2*>(top + kMatvecMaxTokens + 4);
+  uint32_t *const cur = top + kMatvecMaxTokens, *const limit = cur + kMatvecMaxTokens;
+  uint32_t* const next = limit + kMatvecMaxTokens;
+  float2* factors = reinterpret_cast<float2*>(next + kMatvecMaxTokens);
+  uint32_t* wide = top + kTokenWords - 4;
   uint8_t* first = reinterpret_cast<uint8_t*>(top + kTokenWords);  // per tile: first and last warp
   uint8_t* last = first + p.batch;
   float* part = reinterpret_cast<float*>(first + (2 * p.batch + 15) / 16 * 16);  // slot of (tile, warp): tile + warp
@@ -461,7 +483,7 @@ __device__ __forceinline__ bool matvec_body(const Params& p) {
   const int whole = min(chunks, row_bytes / Ring::kRow - chunk0);
   const int64_t group_bytes = static_cast<int64_t>(p.atoms) * 512;
   const int N = static_cast<int>(p.a.N);
-  if (!BF16 && threadIdx.x <= kMatvecMaxTokens) top[threadIdx.x] = 0u;
+  if (threadIdx.x < kMatvecMaxTokens) top[threadIdx.x] = *wide = 0u;
 
   // Load side: walks the items of this warp, batch after batch, kDepth ahead of the other.
   // A lane copies 16-byte pieces of row quarter lq, with WORDS 8 of one row per copy, with
@@ -561,13 +583,11 @@ __device__ __forceinline__ bool matvec_body(const Params& p) {
     }
     copies_commit();  // (empty past the end: the wait counts groups)
   };
-  if (!BF16 && p.split > 1 && !p.sums_over_x) cluster_arrive();  // waited for before the first store into another CTA
-  if (!BF16) __syncthreads();  // `top` is zeroed
+  if (p.split > 1 && !p.sums_over_x) cluster_arrive();  // waited for before the first store into another CTA
+  __syncthreads();  // `top` is zeroed
   segment();
-  if (!BF16) {
-    grid_dependency_wait();
-    grid_dependents_launch();
-  }
+  grid_dependency_wait();
+  grid_dependents_launch();
   const Stager<MX, WORDS> stager{p, u0, un * M, xs};
   stager.fetch();
 #pragma unroll 1
@@ -575,30 +595,19 @@ __device__ __forceinline__ bool matvec_body(const Params& p) {
   copies_wait<kDepth>();  // x, not yet the weights
   // (a loop for each kind of x: 8 tokens of MXFP8, 4096 x 14336 MXFP4, 13.5 us instead of 14.1)
   const bool mx8 = p.a.x_scales != nullptr;
-  if constexpr (BF16) {
-    if (mx8)
-      stager.template stage<true, true>(top);
-    else
-      stager.template stage<false, true>(top);
+  bool far;
+  if (mx8) {
+    stager.template find_top<true>(top);
     __syncthreads();
+    far = stager.template stage<true>(top);
   } else {
-    bool far;
-    if (mx8) {
-      stager.template find_top<true>(top);
-      __syncthreads();
-      far = stager.template stage<true, false>(top);
-    } else {
-      stager.template find_top<false>(top);
-      __syncthreads();
-      far = stager.template stage<false, false>(top);
-    }
-    if (far) top[kMatvecMaxTokens] = 1u;
-    __syncthreads();  // (with a reduction of the flag: 16 tokens, 5376 x 21504, 0.4 us slower)
-    if (top[kMatvecMaxTokens] != 0u) {
-      copies_wait<0>();  // the ring is to be filled again
-      return true;
-    }
+    stager.template find_top<false>(top);
+    __syncthreads();
+    far = stager.template stage<false>(top);
   }
+  if (far) *wide = 1u;
+  __syncthreads();  // (with a reduction of the flag: 16 tokens, 5376 x 21504, 0.4 us slower)
+  const bool many = *wide != 0u;  // passes over the weights
 
   // Compute side: a lane's places in a slot of the ring and in x (a token that is not there
   // repeats the last one: its sums are not kept).
@@ -611,115 +620,118 @@ __device__ __forceinline__ bool matvec_body(const Params& p) {
     x_at[n] = smem_u32(xs + m * 32 + t);
     x_flip[n] = (m & 1) * 64;
   }
-  // What the sums of each token are multiplied by, read after the items' barrier: the tensor scale (gated:
-  // also the gate's) and the power of two that x was scaled down by.
-  if (threadIdx.x < (GATED ? 2 : 1) * kMatvecMaxTokens) {
-    const float* gs = GATED && threadIdx.x >= kMatvecMaxTokens ? p.a.gate.gs : p.a.w.gs;
-    const float sg = gs ? *gs : 1.0f;
-    factors[threadIdx.x] = two_factors(
-        sg, BF16 ? -bf16_exponent<MX>(sg) : down_exponent<MX>(top[threadIdx.x % kMatvecMaxTokens]) + kScaleShift<MX>);
-  }
-  // BF16: what brings the codes back from 2^-126, less the sums' 2^e: with the block scales of rows g and
-  // rows g + 8 for NVFP4, by itself for MXFP4
-  uint32_t back_a = 0, back_b = 0;
-  if constexpr (BF16) {
-    back_b = exp2_bf16x2(126 + bf16_exponent<MX>(p.a.w.gs ? *p.a.w.gs : 1.0f));
-    back_a = GATED ? exp2_bf16x2(126 + bf16_exponent<MX>(p.a.gate.gs ? *p.a.gate.gs : 1.0f)) : back_b;
-  }
+  // What the sums of each token are multiplied by: the tensor scale (gated: also the gate's) and the power of
+  // two that x was scaled down by; by the first threads, from their token's largest magnitude.
+  auto set_factors = [&](const uint32_t* of) {
+    if (threadIdx.x < (GATED ? 2 : 1) * kMatvecMaxTokens) {
+      const float* gs = GATED && threadIdx.x >= kMatvecMaxTokens ? p.a.gate.gs : p.a.w.gs;
+      factors[threadIdx.x] = two_factors(
+          gs ? *gs : 1.0f, down_exponent<MX>(of[threadIdx.x % kMatvecMaxTokens]) + kScaleShift<MX>);
+    }
+  };
+  if (!many) set_factors(top);
   int at = 0;  // the slot's offset in the ring
   for (int tile0 = T0; tile0 < T1; tile0 += p.batch) {
     const int nt = min(p.batch, T1 - tile0);
     const int items = nt * chunks;
     const int i0 = run_start(items, warp);
-    int todo = run_start(items, warp + 1) - i0;
-    int ti = i0 / chunks, c = i0 - ti * chunks;
-    while (todo > 0) {
-      const int stop = min(chunks, c + todo);
-      todo -= stop - c;
-      if (lane == 0) {
-        if (c == 0) first[ti] = static_cast<uint8_t>(warp);
-        if (stop == chunks) last[ti] = static_cast<uint8_t>(warp);
-      }
-      float acc[R][NT][4];
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.0f;
-#pragma unroll 1
-      for (; c < stop; ++c) {
-        copies_wait<kDepth - 1>();
-        __syncwarp();  // every lane's copies of this item have landed
-        uint32_t wa[R][WORDS], wb[R][WORDS];
-        uint32_t ha[R][WORDS / 2], hb[R][WORDS / 2];  // NVFP4: block scales (BF16: times 2^(126 + e)), twice each
-        float fa[R][WORDS], fb[R][WORDS];             // MXFP4: block scales
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint32_t src = codes_at + at + r * 16 * Ring::kRow, ssrc = scales_at + at + r * 64;
-          if constexpr (MX) {
-            // word j: lane t's word of the chunk's block j
-#pragma unroll
-            for (int j = 0; j < WORDS; j += 2) ldmatrix4(src ^ (j << 4), wa[r][j], wb[r][j], wa[r][j + 1], wb[r][j + 1]);
-#pragma unroll
-            for (int h = 0; h < WORDS / 4; ++h) {
-              const uint32_t sca = ld_shared4(ssrc + 64 * R * h), scb = ld_shared4(ssrc + 64 * R * h + 32);
-              const uint32_t by = exp2_bf16x2(BF16 ? 0 : -kScaleShift<MX>);
-              e8m0x2_to_float(sca & 0xFFFFu, by, fa[r][4 * h], fa[r][4 * h + 1]);
-              e8m0x2_to_float(sca >> 16, by, fa[r][4 * h + 2], fa[r][4 * h + 3]);
-              e8m0x2_to_float(scb & 0xFFFFu, by, fb[r][4 * h], fb[r][4 * h + 1]);
-              e8m0x2_to_float(scb >> 16, by, fb[r][4 * h + 2], fb[r][4 * h + 3]);
-            }
-          } else {
-            // word j: codes 8 j .. of the lane's own 32 (16) bytes of the row
-#pragma unroll
-            for (int i = 0; i < WORDS / 4; ++i) {
-              const uint4 a = ld_shared16(src ^ (i << 4));
-              const uint4 b = ld_shared16((src ^ (i << 4)) + 8 * Ring::kRow);
-              wa[r][4 * i] = a.x, wa[r][4 * i + 1] = a.y, wa[r][4 * i + 2] = a.z, wa[r][4 * i + 3] = a.w;
-              wb[r][4 * i] = b.x, wb[r][4 * i + 1] = b.y, wb[r][4 * i + 2] = b.z, wb[r][4 * i + 3] = b.w;
-            }
-            uint32_t sca = ld_shared4(ssrc), scb = ld_shared4(ssrc + 32);
-            if constexpr (WORDS == 4) {
-              sca >>= 16 * (t & 1);
-              scb >>= 16 * (t & 1);
-            }
-#pragma unroll
-            for (int h = 0; h < WORDS / 4; ++h) {
-              uint32_t a2, b2;
-              if constexpr (BF16) {
-                float a0, a1, b0, b1;
-                e4m3x2_to_float((sca >> (16 * h)) & 0xFFFFu, a0, a1);
-                e4m3x2_to_float((scb >> (16 * h)) & 0xFFFFu, b0, b1);
-                a2 = mul_bf16x2(pack_bf16(a0, a1), back_a), b2 = mul_bf16x2(pack_bf16(b0, b1), back_b);
-              } else {
-                a2 = e4m3x2_to_half2((sca >> (16 * h)) & 0xFFFFu), b2 = e4m3x2_to_half2((scb >> (16 * h)) & 0xFFFFu);
-              }
-              ha[r][2 * h] = __byte_perm(a2, 0u, 0x1010), ha[r][2 * h + 1] = __byte_perm(a2, 0u, 0x3232);
-              hb[r][2 * h] = __byte_perm(b2, 0u, 0x1010), hb[r][2 * h + 1] = __byte_perm(b2, 0u, 0x3232);
-            }
-          }
+    bool more = false;
+    int pass = 0;
+    do {
+      if (many) {  // (out of the way of the usual call: as part of its start, 1 token, 14336 x 4096, 10.0 us, not 9.0)
+        copies_wait<0>();
+        ltile = tile0, left = run = at = 0;  // the loads start again with this batch
+        if (threadIdx.x < kMatvecMaxTokens) {
+          uint32_t &c = cur[threadIdx.x], &l = limit[threadIdx.x], &n = next[threadIdx.x];
+          l = pass == 0 ? 0xFFFFFFFFu : n == 0u ? 0u : lowest_exactly(mx8, down_exponent<MX>(c));
+          c = pass == 0 ? top[threadIdx.x] : n;
+          n = 0u;
         }
-        __syncwarp();  // the slot has been read by every lane
-        load(at);
-        at = at == (kDepth - 1) * Ring::kBytes ? 0 : at + Ring::kBytes;
-        const uint32_t xc = (c / kPerUnit) * M * 512 + (c % kPerUnit) * (WORDS * 64);
+        __syncthreads();
+        set_factors(cur);
+        stager.fetch();
+#pragma unroll 1
+        for (int d = 0; d < kDepth; ++d) load(d * Ring::kBytes);
+        copies_wait<kDepth>();
+        stager.stage_below(mx8, cur, limit, next);
+        __syncthreads();
+        more = false;
+        for (int m = 0; m < M; ++m) more = more || next[m] != 0u;
+      }
+      int todo = run_start(items, warp + 1) - i0;
+      int ti = i0 / chunks, c = i0 - ti * chunks;
+      while (todo > 0) {
+        const int stop = min(chunks, c + todo);
+        todo -= stop - c;
+        if (lane == 0) {
+          if (c == 0) first[ti] = static_cast<uint8_t>(warp);
+          if (stop == chunks) last[ti] = static_cast<uint8_t>(warp);
+        }
+        float acc[R][NT][4];
 #pragma unroll
-        for (int j = 0; j < WORDS; ++j) {
-          uint4 x[NT];
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            x[n] = ld_shared16(x_at[n] + xc + (j & 1 ? 0u - x_flip[n] : x_flip[n]) + j * 64);
+          for (int n = 0; n < NT; ++n) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.0f;
+#pragma unroll 1
+        for (; c < stop; ++c) {
+          copies_wait<kDepth - 1>();
+          __syncwarp();  // every lane's copies of this item have landed
+          uint32_t wa[R][WORDS], wb[R][WORDS];
+          uint32_t ha[R][WORDS / 2], hb[R][WORDS / 2];  // NVFP4: block scales, twice each
+          float fa[R][WORDS], fb[R][WORDS];             // MXFP4: block scales
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            uint32_t a[4], b[4];
-            if constexpr (BF16) {
-              codes_to_bf16(wa[r][j], a);
-              codes_to_bf16(wb[r][j], b);
+            const uint32_t src = codes_at + at + r * 16 * Ring::kRow, ssrc = scales_at + at + r * 64;
+            if constexpr (MX) {
+              // word j: lane t's word of the chunk's block j
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] = mul_bf16x2(a[i], MX ? back_a : ha[r][j >> 1]);
-                b[i] = mul_bf16x2(b[i], MX ? back_b : hb[r][j >> 1]);
+              for (int j = 0; j < WORDS; j += 2)
+                ldmatrix4(src ^ (j << 4), wa[r][j], wb[r][j], wa[r][j + 1], wb[r][j + 1]);
+#pragma unroll
+              for (int h = 0; h < WORDS / 4; ++h) {
+                const uint32_t sca = ld_shared4(ssrc + 64 * R * h), scb = ld_shared4(ssrc + 64 * R * h + 32);
+                const uint32_t by = exp2_bf16x2(-kScaleShift<MX>);
+                e8m0x2_to_float(sca & 0xFFFFu, by, fa[r][4 * h], fa[r][4 * h + 1]);
+                e8m0x2_to_float(sca >> 16, by, fa[r][4 * h + 2], fa[r][4 * h + 3]);
+                e8m0x2_to_float(scb & 0xFFFFu, by, fb[r][4 * h], fb[r][4 * h + 1]);
+                e8m0x2_to_float(scb >> 16, by, fb[r][4 * h + 2], fb[r][4 * h + 3]);
               }
             } else {
+              // word j: codes 8 j .. of the lane's own 32 (16) bytes of the row
+#pragma unroll
+              for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 a = ld_shared16(src ^ (i << 4));
+                const uint4 b = ld_shared16((src ^ (i << 4)) + 8 * Ring::kRow);
+                wa[r][4 * i] = a.x, wa[r][4 * i + 1] = a.y, wa[r][4 * i + 2] = a.z, wa[r][4 * i + 3] = a.w;
+                wb[r][4 * i] = b.x, wb[r][4 * i + 1] = b.y, wb[r][4 * i + 2] = b.z, wb[r][4 * i + 3] = b.w;
+              }
+              uint32_t sca = ld_shared4(ssrc), scb = ld_shared4(ssrc + 32);
+              if constexpr (WORDS == 4) {
+                sca >>= 16 * (t & 1);
+                scb >>= 16 * (t & 1);
+              }
+#pragma unroll
+              for (int h = 0; h < WORDS / 4; ++h) {
+                const uint32_t a2 = e4m3x2_to_half2((sca >> (16 * h)) & 0xFFFFu);
+                const uint32_t b2 = e4m3x2_to_half2((scb >> (16 * h)) & 0xFFFFu);
+                ha[r][2 * h] = __byte_perm(a2, 0u, 0x1010), ha[r][2 * h + 1] = __byte_perm(a2, 0u, 0x3232);
+                hb[r][2 * h] = __byte_perm(b2, 0u, 0x1010), hb[r][2 * h + 1] = __byte_perm(b2, 0u, 0x3232);
+              }
+            }
+          }
+          __syncwarp();  // the slot has been read by every lane
+          load(at);
+          at = at == (kDepth - 1) * Ring::kBytes ? 0 : at + Ring::kBytes;
+          const uint32_t xc = (c / kPerUnit) * M * 512 + (c % kPerUnit) * (WORDS * 64);
+#pragma unroll
+          for (int j = 0; j < WORDS; ++j) {
+            uint4 x[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              x[n] = ld_shared16(x_at[n] + xc + (j & 1 ? 0u - x_flip[n] : x_flip[n]) + j * 64);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              uint32_t a[4], b[4];
               codes_to_half(wa[r][j], a);
               codes_to_half(wb[r][j], b);
 #pragma unroll
@@ -727,39 +739,53 @@ __device__ __forceinline__ bool matvec_body(const Params& p) {
                 a[i] = mul_half2(a[i], ha[r][j >> 1]);
                 b[i] = mul_half2(b[i], hb[r][j >> 1]);
               }
-            }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float(&d)[4] = acc[r][n];
-              if constexpr (MX) {
-                float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma<BF16>(q, a[0], b[0], a[1], b[1], x[n].x, x[n].y);
-                mma<BF16>(q, a[2], b[2], a[3], b[3], x[n].z, x[n].w);
-                d[0] = __fmaf_rn(q[0], fa[r][j], d[0]);
-                d[1] = __fmaf_rn(q[1], fa[r][j], d[1]);
-                d[2] = __fmaf_rn(q[2], fb[r][j], d[2]);
-                d[3] = __fmaf_rn(q[3], fb[r][j], d[3]);
-              } else {
-                mma<BF16>(d, a[0], b[0], a[1], b[1], x[n].x, x[n].y);
-                mma<BF16>(d, a[2], b[2], a[3], b[3], x[n].z, x[n].w);
+              for (int n = 0; n < NT; ++n) {
+                float(&d)[4] = acc[r][n];
+                if constexpr (MX) {
+                  float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma(q, a[0], b[0], a[1], b[1], x[n].x, x[n].y);
+                  mma(q, a[2], b[2], a[3], b[3], x[n].z, x[n].w);
+                  d[0] = __fmaf_rn(q[0], fa[r][j], d[0]);
+                  d[1] = __fmaf_rn(q[1], fa[r][j], d[1]);
+                  d[2] = __fmaf_rn(q[2], fb[r][j], d[2]);
+                  d[3] = __fmaf_rn(q[3], fb[r][j], d[3]);
+                } else {
+                  mma(d, a[0], b[0], a[1], b[1], x[n].x, x[n].y);
+                  mma(d, a[2], b[2], a[3], b[3], x[n].z, x[n].w);
+                }
               }
             }
           }
         }
+        float* out = part + (ti + warp) * slot + g;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int m = 8 * n + 2 * t + (i & 1);
+              if (m < M) {
+                float& o = out[(r * M + m) * kPad + 8 * (i >> 1)];
+                float v = acc[r][n][i];
+                if (many) {  // the passes meet under their factors
+                  const float2 f = factors[GATED && i < 2 ? kMatvecMaxTokens + m : m];
+                  v = v * f.x * f.y + (pass == 0 ? 0.0f : o);
+                }
+                o = v;
+              }
+            }
+        c = 0;
+        ++ti;
       }
-      float* out = part + (ti + warp) * slot + g;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int m = 8 * n + 2 * t + (i & 1);
-            if (m < M) out[(r * M + m) * kPad + 8 * (i >> 1)] = acc[r][n][i];
-          }
-      c = 0;
-      ++ti;
-    }
+      if (many) {
+        __syncthreads();  // x, `next` and the factors have been read
+        ++pass;
+        more = more && pass < kMaxPasses;
+        if (!more && threadIdx.x < 2 * kMatvecMaxTokens) factors[threadIdx.x] = make_float2(1.0f, 1.0f);
+      }
+    } while (more);
     __syncthreads();
     // Outputs, four to a thread: i = (group of 16 rows, token, line), the line's rows of the
     // four quarters.
@@ -841,14 +867,6 @@ __device__ __forceinline__ bool matvec_body(const Params& p) {
     }
     __syncthreads();  // the slots may be overwritten
   }
-  return false;
-}
-
-// The two bodies one after the other: with both item loops in one body (1 token, 14336 x 4096) 9.7 us
-// instead of 9.1.
-template <bool MX, int NT, bool GATED, int WORDS, int R>
-__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ Params p) {
-  if (matvec_body<false, MX, NT, GATED, WORDS, R>(p)) matvec_body<true, MX, NT, GATED, WORDS, R>(p);
 }
 
 template <bool MX, int NT, bool GATED, int WORDS, int R>
