@@ -12,6 +12,9 @@ along K, one E4M3 scale per block, one FP32 scale per tensor; absmax or MSE
 block scales) and "NVFP4 en difusión: la misma cuantización, un motor
 completamente distinto", section 2 (packed (out, in/2) codes, (out, in/16)
 scales, out = (A s_a)(B s_b)^T in BF16, activations quantized on every call).
+
+Every call serves inference: nothing here has a gradient, and results are detached
+from tensors that require one.
 """
 from __future__ import annotations
 
@@ -519,7 +522,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
 
     out_format: "bf16" -> a tensor, "mxfp8" -> MXFP8Tensor, "mxfp4" -> MXFP4Tensor, "nvfp4" -> NVFP4Tensor, whose
     tensor scale is `global_scale` (a device float) or computed from v.  Returns the output, or with a residual
-    (output, h); residual_out may be `residual` itself to update the stream in place."""
+    (output, h); residual_out may be `residual` itself to update the stream in place.  No gradient: the results are
+    detached."""
     fmt, lay = _choices(out_format, layout)
     ld_x = _ld(x, "x")
     dev = x.get_device()
@@ -557,7 +561,8 @@ def silu_mul(gate: torch.Tensor, up: torch.Tensor, out_format: str = "bf16", lay
              global_scale: Optional[torch.Tensor] = None, out=None, workspace: Optional[torch.Tensor] = None,
              stream=None):
     """silu(gate) * up of two 2-D BF16 tensors (strided views, such as the halves of one product, are fine), written
-    as `out_format` like rms_norm's output (see nvfp4_silu_mul in include/nvfp4.h)."""
+    as `out_format` like rms_norm's output (see nvfp4_silu_mul in include/nvfp4.h).  No gradient: the result is
+    detached."""
     fmt, lay = _choices(out_format, layout)
     ld_g = _ld(gate, "gate")
     dev = gate.get_device()
@@ -579,7 +584,7 @@ def matvec(x, w, w_gate=None, out: Optional[torch.Tensor] = None, stream=None) -
     """y = x w^T in BF16 for up to MATVEC_MAX_TOKENS rows of x (2-D BF16 tensor, or MXFP8Tensor) and a 4-bit weight w
     (NVFP4Tensor or MXFP4Tensor, N x K, swizzled scales); the activation is not rounded to 4 bits.  With w_gate, a
     second weight of the same kind and shape: silu(x w_gate^T) * (x w^T) in one pass.  More rows: use linear,
-    nvfp4_gemm or mxfp4_gemm."""
+    nvfp4_gemm or mxfp4_gemm.  No gradient: the result is detached."""
     if isinstance(x, torch.Tensor):
         data, scales, x_lay, ld_x = x, None, SF_SWIZZLED, _ld(x, "x")
         M, K = x.shape
