@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       const float ss[4] = {s.x, s.y, s.z, s.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float f = GATED ? silu_times(ss[k], vv[k]) : ss[k];
+        const float f = GATED ? silu_times_short(ss[k], vv[k]) : ss[k];
         if (row + 32 * k < N) y[32 * k] = static_cast<uint16_t>(pack_bf16(f, 0.0f));
       }
     };
