@@ -181,3 +181,34 @@ def test_mxfp8_values_down_to_the_smallest(cuda_device):
     w0 = nv.MXFP4Tensor(zero_first, w.scales, N, K)
     y, bound = ref.matvec64(values(x), w0)
     ref.check_product(nv.matvec(x, w0), y, bound)
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", [(4, 40, 2304), (12, 130, 4096)])
+def test_non_finite_values_beside_small_ones(cuda_device, kind, M, N, K):
+    """Infinities and NaN in calls that take several passes: they stay in their token and their formula."""
+    x, w = banded(M, N, K, kind, 1, np.arange(-90, 60), 5)
+    clean = nv.matvec(x, w)
+    z = x.clone()
+    z[1, 77] = float("inf")
+    z[2, 2200] = float("nan")
+    got = nv.matvec(z, w)
+    keep = [i for i in range(M) if i not in (1, 2)]
+    assert torch.equal(got[keep], clean[keep])
+    assert got[2].isnan().all()
+    col = ref.dequantize64(w)[:, 77]
+    want = np.where(col == 0, np.nan, np.copysign(np.inf, col))
+    assert np.array_equal(got[1].double().cpu().numpy(), want, equal_nan=True)
+
+
+def test_tokens_of_zeros_and_of_one_value_beside_wide_ones(cuda_device):
+    """Tokens that are through after no pass, one and several, in one call."""
+    x, w = banded(9, 77, 1088, "nvfp4", 1, np.arange(-100, 60), 8)
+    x[0] = 0
+    x[3] = 0
+    x[3, 1000] = 2.0 ** -70
+    x[5] = 1.5
+    y, bound = ref.matvec64(x, w)
+    got = nv.matvec(x, w)
+    ref.check_product(got, y, bound)
+    assert (got[0] == 0).all()
