@@ -74,3 +74,15 @@ def test_gated_product_of_far_negative_gates(cuda_device):
     # one product per sum: the gate is off by 3 roundings, so e^gate by 99 * 3 * 2^-24, and BF16 by half a step
     got = nv.matvec(x, up, gate).double().cpu().numpy()
     assert (np.abs(got - y) <= np.abs(y) * (2.0 ** -8 + 2.0 ** -14)).all()
+
+
+@pytest.mark.parametrize("power", [-133, -126, 0, 127])
+def test_norm_of_one_value_in_a_row_of_millions(cuda_device, power):
+    """One value among 2^22 zeros, down to BF16's smallest: the mean square goes to 2^-288."""
+    cols = 2 ** 22 + 3
+    x = torch.zeros((1, cols), dtype=torch.bfloat16, device="cuda")
+    x[0, 12345] = 2.0 ** power
+    y = nv.rms_norm(x, eps=0.0).double().cpu().numpy()
+    v = np.zeros((1, cols))
+    v[0, 12345] = np.sqrt(cols)
+    assert np.count_nonzero(y) == 1 and abs(y[0, 12345] - v[0, 12345]) <= v[0, 12345] * 2.0 ** -8

@@ -547,8 +547,9 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_
       s = __fma_rn(f, f, s);
     }
     const double m = block_sum(s, sums) / static_cast<double>(a.cols) + static_cast<double>(a.eps);
-    const int f = m > 0x1p100 && m < 0x1p300 ? -80 : m < 0x1p-100 ? 80 : 0;
-    const InvRms inv = inv_rms(static_cast<float>(m * (f < 0 ? 0x1p-160 : f > 0 ? 0x1p160 : 1.0)), f);
+    // (down to 2^-266 over 2^31 columns)
+    const int f = m > 0x1p100 && m < 0x1p300 ? -100 : m < 0x1p-100 ? 100 : 0;
+    const InvRms inv = inv_rms(static_cast<float>(m * (f < 0 ? 0x1p-200 : f > 0 ? 0x1p200 : 1.0)), f);
     const uint16_t* h = q ? ho : x;
     for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) finish(c, bf16_bits_to_float(h[c]), inv);
   }
