@@ -78,15 +78,6 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
   return d;
 }
 
-// The sixteen BF16 values of a thread's unit as floats.
-__device__ __forceinline__ void widen(const uint32_t (&w)[8], float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-
 // A unit is one 32-byte access where every row starts at a multiple of 32 bytes (`wide`),
 // else two of 16 (8192 x 5376 to MXFP8 47.7 against 50.7 us).
 __device__ __forceinline__ void load_unit(const uint16_t* p, bool wide, uint32_t (&w)[8]) {
@@ -559,7 +550,7 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a, uint16_
 // 16-byte boundary, the same in every matrix, so that the row is read and written in the
 // 16-byte vectors that cover it; the two at its ends go value by value.  The weight, which
 // does not share that shift, is read in words and shifted by half a word for odd s.
-// (8192 x 5375 with a residual: 73 us; value by value 162.)
+// (8192 x 5375 with a residual: 74 us; value by value 162.)
 template <int V>
 __global__ void __launch_bounds__(512) norm_dense_kernel(const NormArgs a, uint16_t* out) {
   __shared__ float sums[2][32];
