@@ -129,7 +129,7 @@ def test_values_of_any_magnitude_handled_token_by_token(cuda_device, kind):
 @pytest.mark.parametrize("power", [-120, -60, 60, 109])
 @pytest.mark.parametrize("spread", [False, True])
 def test_mxfp4_weights_of_any_magnitude(cuda_device, power, spread):
-    """Weights up to 2^110, in both forms of x: near one another and 40 binades apart."""
+    """Weights up to 2^110, values of x near one another and 40 binades apart (one pass and two)."""
     M, N, K = 8, 130, 1056
     x = bf16((M, K), 1).float()
     x = torch.ldexp(x, torch.full((), 100 if power == -120 else -3, device="cuda"))
@@ -143,7 +143,7 @@ def test_mxfp4_weights_of_any_magnitude(cuda_device, power, spread):
 
 @pytest.mark.parametrize("scale", [-30, -15, -9, 0, 20])
 def test_nvfp4_tensor_scales_of_any_magnitude(cuda_device, scale):
-    """The tensor scale's power of two goes with the codes in the BF16 form, as far as it fits there."""
+    """Passes meet under their own factors, of which the tensor scale is a part."""
     x, w = banded(3, 77, 544, "nvfp4", 1, np.arange(-60, 41), 9)
     w.global_scale.fill_(1.37 * 2.0 ** scale)
     y, bound = ref.matvec64(x, w)
